@@ -348,6 +348,109 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
                                  int Dk, int Dv, gdn2_dtype dt, void* stream);
 
 /*
+ * Linear attention with one fixed decay per head -- the recurrence without
+ * erase and write gates, whose decay is a property of the head:
+ *
+ *     S_t = a_h S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_h = exp(log_decay_h)
+ *
+ *   q, k, dq, dk       : [B, T, H, Dk] dt ;  v, o, dout, dv : [B, T, H, Dv] dt
+ *   log_decay          : [H] float32, DEVICE memory, any value <= 0: 0 is plain
+ *                        linear attention, -inf a head without memory. It has no
+ *                        gradient (a head's decay is set, not learned). Positive
+ *                        values are accepted while a_h^128 stays finite.
+ *   S0, ST, dST, dS0   : [B, H, Dk, Dv] float32, nullable: S0 and dST read as
+ *                        zero, ST and dS0 are then not written. ST may alias S0,
+ *                        and dS0 dST.
+ * gdn2_linear_bwd gives the gradients of <dout, o> + <dST, S_T> from the
+ * forward's inputs alone (nothing is kept by the forward); the three token
+ * gradients must be given and must not alias the inputs.
+ * Dk, Dv in {16, 32, 64, 128}, float32 or bf16, any T >= 0.
+ * NaN and infinity in a token reach every output of the chunk of 128 tokens it
+ * lies in, earlier ones too, and the states behind it (before it, for the
+ * backward); they never reach another sequence.
+ * Packed sequences (the varlen calls): token tensors [Ttot, H, D] and
+ * cu_seqlens [N + 1] int32 in device memory, as for gdn2_varlen_fwd, but read
+ * and written in place: nothing is padded. A sequence of no tokens hands S0 to
+ * ST. Rows behind the last sequence are not written. A sequence longer than
+ * Tmax is cut at Tmax, one outside [0, Ttot) is skipped, and
+ * gdn2_device_status then returns GDN2_ERR_INVALID with the detail
+ * "cu_seqlens".
+ * Workspace: gdn2_linear_workspace_size(GDN2_OP_FWD or GDN2_OP_BWD, ...) bytes,
+ * 256-byte aligned, with N = B and T for a dense call, N and Tmax for a packed
+ * one; nothing in it outlives the call. 0 for another op or an invalid problem.
+ */
+size_t gdn2_linear_workspace_size(gdn2_op op, int N, int T, int H, int Dk, int Dv, gdn2_dtype dt);
+gdn2_status gdn2_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
+                            void* o, float* ST, int B, int T, int H, int Dk, int Dv, gdn2_dtype dt, void* ws,
+                            size_t ws_bytes, void* stream);
+gdn2_status gdn2_linear_bwd(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
+                            const void* dout, const float* dST, void* dq, void* dk, void* dv, float* dS0, int B,
+                            int T, int H, int Dk, int Dv, gdn2_dtype dt, void* ws, size_t ws_bytes, void* stream);
+gdn2_status gdn2_linear_varlen_fwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const int* cu_seqlens, int N, int Tmax, long long Ttot, const float* S0, void* o,
+                                   float* ST, int H, int Dk, int Dv, gdn2_dtype dt, void* ws, size_t ws_bytes,
+                                   void* stream);
+gdn2_status gdn2_linear_varlen_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                                   const int* cu_seqlens, int N, int Tmax, long long Ttot, const float* S0,
+                                   const void* dout, const float* dST, void* dq, void* dk, void* dv, float* dS0,
+                                   int H, int Dk, int Dv, gdn2_dtype dt, void* ws, size_t ws_bytes, void* stream);
+/*
+ * One token of it for every request of a batch, on a pool of states:
+ *   q, k : [B, H, Dk] dt ;  v, o : [B, H, Dv] dt ;  log_decay : [H] float32
+ *   S     : [num_slots, H, Dk, Dv] float32, the named states updated in place
+ *   slots : [B] int32, DEVICE memory: the state of each row; NULL: row b has S[b]
+ * A row whose slot is negative is idle: no state is touched and its o is zero.
+ * So is a row whose slot lies outside the pool or was named by an earlier row
+ * (a state takes one token a step), and gdn2_device_status then returns
+ * GDN2_ERR_INVALID with the detail "slots".
+ */
+gdn2_status gdn2_linear_decode_step(const void* q, const void* k, const void* v, const float* log_decay, float* S,
+                                    const int* slots, int num_slots, void* o, int B, int H, int Dk, int Dv,
+                                    gdn2_dtype dt, void* stream);
+
+/*
+ * RMS norm of every query and key head and the rotation of its channel pairs by
+ * the token's position, in one pass. Per head row x of D channels
+ *     n = x * weight / sqrt(mean(x^2) + eps)       (norm = 0: n = x)
+ * and for pair p < pairs, at the angle t = positions[axes[p]][token] * inv_freq[p],
+ *     (y_a, y_b) = (n_a cos t - n_b sin t, n_a sin t + n_b cos t)
+ * with the pair's channels a = p, b = p + pairs, or a = 2p, b = 2p + 1
+ * (interleaved nonzero); channels from 2 pairs on are n.
+ *   q, k           : rows [B * T] of Hq x D and Hk x D dt, each token's heads
+ *                    contiguous and tokens q_stride / k_stride elements apart
+ *                    (a multiple of 16 bytes): parts of one projection's output
+ *                    are taken where they lie
+ *   q_out, k_out   : [B, T, Hq, D] and [B, T, Hk, D] dt; may be q and k where
+ *                    those are contiguous (each row is read before it is written)
+ *   positions      : [num_axes, B, T] int32 (pos_bytes = 4) or int64 (8), any value
+ *   inv_freq       : [pairs] float32 ;  axes : [pairs] int32 or NULL (all 0)
+ *   pairs          : 1 .. D / 2
+ *   q_weight, k_weight : [D] float32, or NULL for a norm without a weight
+ * The angle is reduced in 64 bits, so far positions turn as exactly as near
+ * ones. An axis outside [0, num_axes) turns nothing and is reported by
+ * gdn2_device_status (GDN2_ERR_INVALID, "axes"). D in {16, 32, 64, 128}. An L2
+ * norm x / sqrt(sum(x^2) + e) is the weight 1 / sqrt(D) with eps = e / D.
+ *
+ * gdn2_qk_norm_rope_bwd: dq, dk (contiguous, as the outputs; they may be dq_out
+ * and dk_out) from the forward's inputs and the outputs' gradients, and with a
+ * norm the weights' gradients [D] float32, summed over tokens and heads in a
+ * fixed order (NULL: not wanted). Its workspace, gdn2_qk_norm_rope_workspace_size
+ * bytes (256-byte aligned), is needed for the weights' gradients only.
+ */
+size_t gdn2_qk_norm_rope_workspace_size(int D);
+gdn2_status gdn2_qk_norm_rope_fwd(const void* q, const void* k, long long q_stride, long long k_stride,
+                                  const void* positions, int pos_bytes, int num_axes, const float* inv_freq,
+                                  const int* axes, int pairs, int interleaved, int norm, float eps,
+                                  const float* q_weight, const float* k_weight, void* q_out, void* k_out, int B, int T,
+                                  int Hq, int Hk, int D, gdn2_dtype dt, void* stream);
+gdn2_status gdn2_qk_norm_rope_bwd(const void* q, const void* k, long long q_stride, long long k_stride,
+                                  const void* dq_out, const void* dk_out, const void* positions, int pos_bytes,
+                                  int num_axes, const float* inv_freq, const int* axes, int pairs, int interleaved,
+                                  int norm, float eps, const float* q_weight, const float* k_weight, void* dq,
+                                  void* dk, float* dq_weight, float* dk_weight, int B, int T, int Hq, int Hk, int D,
+                                  gdn2_dtype dt, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Per-kernel timing, for profiling. gdn2_trace_enable(1) makes every later
  * kernel launch of the library record a CUDA event before and after it on the
  * launch's stream (gdn2_trace_enable(0) stops it; off by default).
@@ -368,7 +471,8 @@ int gdn2_trace_read(char* names, size_t names_cap, int* launches, double* ms, in
  * an event was recorded since the previous call (gdn2_last_error names the
  * kernel and the kind of wait) and clears the record; GDN2_ERR_CUDA if the
  * stream holds a CUDA error, and GDN2_ERR_INVALID if a packed-sequence call met
- * an inconsistent cu_seqlens (see gdn2_varlen_fwd). The entry points above never
+ * an inconsistent cu_seqlens (see gdn2_varlen_fwd), a decode step a bad slot
+ * (gdn2_linear_decode_step) or a rotation a bad axis (gdn2_qk_norm_rope_fwd). The entry points above never
  * synchronise, so this is the call that checks a finished step after the fact.
  */
 gdn2_status gdn2_device_status(void* stream);

@@ -8,7 +8,9 @@ loads it on first use and raises if it is missing.
 """
 
 __all__ = ["gdn2_fwd", "gdn2_bwd", "gdn2_decode_step", "gdn2_workspace_size", "gated_delta_rule2",
-           "GatedDeltaRule2", "Gdn2Error"]
+           "GatedDeltaRule2", "Gdn2Error", "gdn2_linear_fwd", "gdn2_linear_bwd", "gdn2_linear_varlen_fwd",
+           "gdn2_linear_varlen_bwd", "gdn2_linear_decode_step", "decay_linear_attention", "gdn2_qk_norm_rope_fwd",
+           "gdn2_qk_norm_rope_bwd", "qk_norm_rope"]
 
 
 def __getattr__(name):

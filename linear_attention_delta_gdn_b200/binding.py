@@ -35,7 +35,10 @@ EXPORTS = ("gdn2_workspace_size", "gdn2_fwd", "gdn2_bwd", "gdn2_decode_step", "g
            "gdn2_last_error", "gdn2_version", "gdn2_bwd_no_alloc", "gdn2_no_alloc_scratch_bytes",
            "gdn2_trace_enable", "gdn2_trace_read", "gdn2_device_status", "gdn2_beta_workspace_size",
            "gdn2_beta_fwd", "gdn2_beta_bwd", "gdn2_varlen_workspace_size", "gdn2_varlen_fwd", "gdn2_varlen_bwd",
-           "gdn2_fwd_map", "gdn2_bwd_map", "gdn2_state_affine", "gdn2_layer_gates_fwd", "gdn2_layer_gates_bwd")
+           "gdn2_fwd_map", "gdn2_bwd_map", "gdn2_state_affine", "gdn2_layer_gates_fwd", "gdn2_layer_gates_bwd",
+           "gdn2_linear_workspace_size", "gdn2_linear_fwd", "gdn2_linear_bwd", "gdn2_linear_varlen_fwd",
+           "gdn2_linear_varlen_bwd", "gdn2_linear_decode_step", "gdn2_qk_norm_rope_workspace_size",
+           "gdn2_qk_norm_rope_fwd", "gdn2_qk_norm_rope_bwd")
 GDN2_GATE_KDA, GDN2_GATE_GDN = 1, 2
 
 
@@ -96,6 +99,26 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
     L.gdn2_layer_gates_fwd.restype = I
     L.gdn2_layer_gates_bwd.argtypes = [P] * 9 + [I] * 6 + [P]
     L.gdn2_layer_gates_bwd.restype = I
+    F = ctypes.c_float
+    L.gdn2_linear_workspace_size.argtypes = [I] * 7
+    L.gdn2_linear_workspace_size.restype = Z
+    L.gdn2_linear_fwd.argtypes = [P] * 7 + [I] * 6 + [P, Z, P]
+    L.gdn2_linear_fwd.restype = I
+    L.gdn2_linear_bwd.argtypes = [P] * 11 + [I] * 6 + [P, Z, P]
+    L.gdn2_linear_bwd.restype = I
+    L.gdn2_linear_varlen_fwd.argtypes = [P] * 5 + [I, I, LL] + [P] * 3 + [I] * 4 + [P, Z, P]
+    L.gdn2_linear_varlen_fwd.restype = I
+    L.gdn2_linear_varlen_bwd.argtypes = [P] * 5 + [I, I, LL] + [P] * 7 + [I] * 4 + [P, Z, P]
+    L.gdn2_linear_varlen_bwd.restype = I
+    L.gdn2_linear_decode_step.argtypes = [P] * 6 + [I, P] + [I] * 5 + [P]
+    L.gdn2_linear_decode_step.restype = I
+    L.gdn2_qk_norm_rope_workspace_size.argtypes = [I]
+    L.gdn2_qk_norm_rope_workspace_size.restype = Z
+    rope = [P, I, I, P, P, I, I, I, F, P, P]   # positions .. k_weight
+    L.gdn2_qk_norm_rope_fwd.argtypes = [P, P, LL, LL] + rope + [P] * 2 + [I] * 6 + [P]
+    L.gdn2_qk_norm_rope_fwd.restype = I
+    L.gdn2_qk_norm_rope_bwd.argtypes = [P, P, LL, LL, P, P] + rope + [P] * 4 + [I] * 6 + [P, Z, P]
+    L.gdn2_qk_norm_rope_bwd.restype = I
     L.gdn2_device_status.argtypes = [P]
     L.gdn2_device_status.restype = I
     L.gdn2_trace_enable.argtypes = [I]
@@ -402,6 +425,324 @@ def gdn2_decode_step(q, k, v, log_alpha, b, w, S, o=None):
     return o
 
 
+# ------------------------------------------------------------------ linear attention with a decay per head
+
+def _on(t: torch.Tensor, device, name: str):
+    """Device pointer of a contiguous tensor on the call's device (as an int: ctypes converts it by the argtypes)."""
+    if t.device != device:
+        raise ValueError("%s must be on %s, not on %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _opt(t: Optional[torch.Tensor], device, name: str, dtype, shape):
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError("%s must be %s %s" % (name, dtype, list(shape)))
+    return _on(t, device, name)
+
+
+class _Device:
+    """The call's device made current (launches go to the current device) and its current stream."""
+
+    def __init__(self, t: torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        self.device = t.device
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int, dt: int) -> int:
+    return int(lib().gdn2_linear_workspace_size(op, N, T, H, Dk, Dv, dt))
+
+
+def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs, ends):
+    """Shared by the four whole-sequence calls: checks, outputs, workspace, the call. Returns (outs, end state)."""
+    packed = cu is not None
+    lead = tuple(q.shape[:-2])
+    if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
+        raise ValueError("q and v must be [%sH, D]" % ("Ttot, " if packed else "B, T, "))
+    H, Dk = q.shape[-2:]
+    Dv = v.shape[-1]
+    dev, dt, code = q.device, q.dtype, _dt(q)
+    for name, t, D in (("k", k, Dk), ("v", v, Dv)) + ((("dout", dout, Dv),) if dout is not None else ()):
+        if t.dtype != dt or tuple(t.shape) != lead + (H, D):
+            raise ValueError("%s must be %s %s" % (name, dt, list(lead + (H, D))))
+    if log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (H,):
+        raise ValueError("log_decay must be float32 [%d]" % H)
+    if packed:
+        if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError("cu_seqlens must be int32 [N + 1]")
+        N, T = cu.numel() - 1, int(Tmax)
+    else:
+        N, T = lead
+    bwd = dout is not None
+    state = (N, H, Dk, Dv)
+    with _Device(q) as stream:
+        made = []
+        for name, t, like in outs:
+            if t is None:
+                t = torch.empty_like(like, memory_format=torch.contiguous_format)
+            elif t.dtype != dt or t.shape != like.shape:
+                raise ValueError("%s must be %s %s" % (name, dt, list(like.shape)))
+            made.append(t)
+        name, end = ends
+        if end is None and want_end:
+            end = torch.empty(state, dtype=torch.float32, device=dev)
+        need = lib().gdn2_linear_workspace_size(GDN2_OP_BWD if bwd else GDN2_OP_FWD, N, T, H, Dk, Dv, code)
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        f32 = torch.float32
+        args = [_on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay")]
+        if packed:
+            args += [_on(cu, dev, "cu_seqlens"), N, T, lead[0]]
+        args.append(_opt(S0, dev, "S0", f32, state))
+        if bwd:
+            args += [_on(dout, dev, "dout"), _opt(dST, dev, "dST", f32, state)]
+        args += [_on(t, dev, o[0]) for t, o in zip(made, outs)]
+        args.append(_opt(end, dev, name, f32, state))
+        if not packed:
+            args += [N, T]
+        rc = getattr(lib(), fn)(*args, H, Dk, Dv, code, None if ws is None else _on(ws, dev, "ws"),
+                                0 if ws is None else ws.numel() * ws.element_size(), stream)
+    _check(fn, rc)
+    return made, end
+
+
+def gdn2_linear_fwd(q, k, v, log_decay, S0=None, want_state: bool = True, ws: Optional[torch.Tensor] = None, o=None, ST=None):
+    """Linear attention with a fixed decay per head, ``S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T``, ``o_t = S_t^T q_t``.
+
+    q, k [B, T, H, Dk], v [B, T, H, Dv] (bf16 or fp32), log_decay [H] fp32 (<= 0), S0 [B, H, Dk, Dv] fp32 or None.
+    Returns ``(o, ST)`` (``ST`` is None unless ``want_state`` or given). ``ws`` is a uint8 CUDA tensor of at least
+    ``gdn2_linear_workspace_size(GDN2_OP_FWD, ...)`` bytes, allocated if not given.
+    """
+    (o,), ST = _linear("gdn2_linear_fwd", q, k, v, log_decay, S0, None, None, None, None, want_state, ws,
+                       (("o", o, v),), ("ST", ST))
+    return o, ST
+
+
+def gdn2_linear_bwd(q, k, v, log_decay, dout, S0=None, dST=None, want_dS0: bool = True,
+                    ws: Optional[torch.Tensor] = None, grads=None):
+    """Backward of :func:`gdn2_linear_fwd` for L = <dout, o> + <dST, S_T>: dict with dq, dk, dv (input dtype) and dS0
+    (fp32 or None)."""
+    g = grads or {}
+    (dq, dk, dv), dS0 = _linear("gdn2_linear_bwd", q, k, v, log_decay, S0, dout, dST, None, None, want_dS0, ws,
+                                (("dq", g.get("dq"), q), ("dk", g.get("dk"), k), ("dv", g.get("dv"), v)),
+                                ("dS0", g.get("dS0")))
+    return {"dq": dq, "dk": dk, "dv": dv, "dS0": dS0}
+
+
+def gdn2_linear_varlen_fwd(q, k, v, log_decay, cu_seqlens, Tmax: int, S0=None, want_state: bool = True,
+                           ws: Optional[torch.Tensor] = None, o=None, ST=None):
+    """Packed sequences: q, k, v [Ttot, H, D], cu_seqlens int32 [N + 1] on the device, Tmax >= every length.
+    Returns ``(o [Ttot, H, Dv], ST [N, H, Dk, Dv] or None)``; rows of ``o`` behind the last sequence are not written."""
+    (o,), ST = _linear("gdn2_linear_varlen_fwd", q, k, v, log_decay, S0, None, None, cu_seqlens, Tmax, want_state, ws,
+                       (("o", o, v),), ("ST", ST))
+    return o, ST
+
+
+def gdn2_linear_varlen_bwd(q, k, v, log_decay, dout, cu_seqlens, Tmax: int, S0=None, dST=None, want_dS0: bool = True,
+                           ws: Optional[torch.Tensor] = None, grads=None):
+    """Backward of :func:`gdn2_linear_varlen_fwd`: dict of packed dq, dk, dv and dS0 [N, ...]."""
+    g = grads or {}
+    (dq, dk, dv), dS0 = _linear("gdn2_linear_varlen_bwd", q, k, v, log_decay, S0, dout, dST, cu_seqlens, Tmax, want_dS0, ws,
+                                (("dq", g.get("dq"), q), ("dk", g.get("dk"), k), ("dv", g.get("dv"), v)),
+                                ("dS0", g.get("dS0")))
+    return {"dq": dq, "dk": dk, "dv": dv, "dS0": dS0}
+
+
+def gdn2_linear_decode_step(q, k, v, log_decay, S, slots=None, o=None):
+    """One token of :func:`gdn2_linear_fwd` for every row: q, k, v [B, H, D]; S [num_slots, H, Dk, Dv] fp32, updated in
+    place. ``slots`` (int32 [B] on the device) names each row's state, a negative one an idle row (its o is zero);
+    None: row b has S[b]. Returns o."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and v must be [B, H, D]")
+    B, H, Dk = q.shape
+    Dv = v.shape[-1]
+    dev, dt, code = q.device, q.dtype, _dt(q)
+    if k.dtype != dt or k.shape != q.shape or v.dtype != dt or v.shape[:2] != q.shape[:2]:
+        raise ValueError("k and v must be %s [%d, %d, D]" % (dt, B, H))
+    if log_decay.dtype != torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != H:
+        raise ValueError("log_decay must be float32 [%d]" % H)
+    if S.dtype != torch.float32 or S.dim() != 4 or tuple(S.shape[1:]) != (H, Dk, Dv):
+        raise ValueError("S must be float32 [num_slots, %d, %d, %d]" % (H, Dk, Dv))
+    with _Device(q) as stream:
+        if o is None:
+            o = torch.empty((B, H, Dv), dtype=dt, device=dev)
+        elif o.dtype != dt or tuple(o.shape) != (B, H, Dv):
+            raise ValueError("o must be %s [%d, %d, %d]" % (dt, B, H, Dv))
+        rc = lib().gdn2_linear_decode_step(
+            _on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay"), _on(S, dev, "S"),
+            None if slots is None else _opt(slots, dev, "slots", torch.int32, (B,)), S.shape[0], _on(o, dev, "o"),
+            B, H, Dk, Dv, code, stream)
+    _check("gdn2_linear_decode_step", rc)
+    return o
+
+
+class DecayLinearAttention(torch.autograd.Function):
+    """autograd wrapper of the linear attention calls (dense, or packed with cu_seqlens)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, S0, cu_seqlens, Tmax):
+        ctx.set_materialize_grads(False)
+        if cu_seqlens is None:
+            o, ST = gdn2_linear_fwd(q, k, v, log_decay, S0)
+        else:
+            # rows behind the last sequence are nobody's: zeros, so that what follows can take the whole tensor
+            o, ST = gdn2_linear_varlen_fwd(q, k, v, log_decay, cu_seqlens, Tmax, S0, o=torch.zeros_like(v))
+        ctx.save_for_backward(q, k, v, log_decay, S0, cu_seqlens)
+        ctx.Tmax = Tmax
+        return o, ST
+
+    @staticmethod
+    def backward(ctx, do, dST):
+        q, k, v, log_decay, S0, cu = ctx.saved_tensors
+        if do is None and dST is None:
+            return (None,) * 7
+        do = torch.zeros_like(v) if do is None else do.contiguous()
+        dST = None if dST is None else dST.contiguous()
+        want = ctx.needs_input_grad[4]
+        if cu is None:
+            g = gdn2_linear_bwd(q, k, v, log_decay, do, S0, dST, want_dS0=want)
+        else:
+            grads = {"dq": torch.zeros_like(q), "dk": torch.zeros_like(k), "dv": torch.zeros_like(v)}
+            g = gdn2_linear_varlen_bwd(q, k, v, log_decay, do, cu, ctx.Tmax, S0, dST, want_dS0=want, grads=grads)
+        return g["dq"], g["dk"], g["dv"], None, g["dS0"], None, None
+
+
+def decay_linear_attention(q, k, v, log_decay, S0=None, cu_seqlens=None, Tmax: Optional[int] = None):
+    """Differentiable linear attention with a fixed decay per head. Returns ``(o, S_T)``. With ``cu_seqlens`` (and
+    ``Tmax``) the tensors are packed [Ttot, H, D]; ``o`` and the gradients are zero behind the last sequence."""
+    if log_decay.requires_grad:
+        raise ValueError("log_decay has no gradient: pass it detached")
+    if (cu_seqlens is None) != (Tmax is None):
+        raise ValueError("cu_seqlens and Tmax come together")
+    return DecayLinearAttention.apply(q, k, v, log_decay, S0, cu_seqlens, Tmax)
+
+
+# ------------------------------------------------------------------ query/key norm and rotation
+
+def rope_axes(sections, device="cuda") -> torch.Tensor:
+    """The ``axes`` argument for pairs laid out axis after axis, ``sections[i]`` pairs turning by axis i."""
+    return torch.cat([torch.full((int(n),), i, dtype=torch.int32) for i, n in enumerate(sections)]).to(device)
+
+
+def _rows_of(t, name, B, T, H, D):
+    """Pointer and token stride of [B, T, H, D] whose heads are contiguous and whose tokens are evenly spaced."""
+    if t.stride(3) != 1 and D > 1 or t.stride(2) != D and H > 1 or (B > 1 and T > 1 and t.stride(0) != T * t.stride(1)):
+        raise ValueError("%s: a token's heads must be contiguous and the tokens evenly spaced" % name)
+    return t.data_ptr(), (t.stride(1) if T > 1 else t.stride(0) if B > 1 else H * D)
+
+
+def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved):
+    """Checks of the arguments the forward and the backward share: (sizes, leading and positional C arguments)."""
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("q and k must be [B, T, Hq, D] and [B, T, Hk, D]")
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    dev, dt = q.device, q.dtype
+    if k.dtype != dt or k.device != dev:
+        raise ValueError("q and k must be of one dtype and on one device")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    if positions.dim() not in (2, 3) or tuple(positions.shape[-2:]) != (B, T):
+        raise ValueError("positions must be [B, T] or [axes, B, T] = [..., %d, %d]" % (B, T))
+    num_axes = positions.shape[0] if positions.dim() == 3 else 1
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float32 [pairs]")
+    P = inv_freq.numel()
+    if num_axes > 1 and axes is None:
+        raise ValueError("positions of several axes need axes, the axis of each pair")
+    norm = eps is not None
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("a weight needs a norm: give eps")
+    f32 = torch.float32
+    qp, qs = _rows_of(q, "q", B, T, Hq, D)
+    kp, ks = _rows_of(k, "k", B, T, Hk, D)
+    tail = (_on(positions, dev, "positions"), positions.element_size(), num_axes, _on(inv_freq, dev, "inv_freq"),
+            _opt(axes, dev, "axes", torch.int32, (P,)), P, int(interleaved), int(norm), eps if norm else 0.0,
+            _opt(q_weight, dev, "q_weight", f32, (D,)), _opt(k_weight, dev, "k_weight", f32, (D,)))
+    return (B, T, Hq, Hk, D, _dt(q)), (qp, kp, qs, ks), tail
+
+
+def gdn2_qk_norm_rope_fwd(q, k, positions, inv_freq, axes=None, q_weight=None, k_weight=None, eps: Optional[float] = 1e-6,
+                          interleaved: bool = False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and the rotation of its channel pairs by the token's position.
+
+    q [B, T, Hq, D], k [B, T, Hk, D] (bf16 or fp32; a token's heads contiguous, so slices of one projection's output
+    are taken as they are), positions int32 or int64 [B, T], or [axes, B, T] with ``axes`` (int32 [pairs], see
+    :func:`rope_axes`) naming each pair's axis, inv_freq fp32 [pairs], weights fp32 [D] or None. ``eps=None``: no norm.
+    Pairs are channels (p, p + pairs), or (2p, 2p + 1) if ``interleaved``. Returns ``(q_out, k_out)``, contiguous.
+    """
+    with _Device(q) as stream:
+        sizes, lead, tail = _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        rc = lib().gdn2_qk_norm_rope_fwd(*lead, *tail, _opt(q_out, q.device, "q_out", q.dtype, tuple(q.shape)),
+                                         _opt(k_out, q.device, "k_out", q.dtype, tuple(k.shape)), *sizes, stream)
+    _check("gdn2_qk_norm_rope_fwd", rc)
+    return q_out, k_out
+
+
+def gdn2_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, axes=None, q_weight=None, k_weight=None,
+                          eps: Optional[float] = 1e-6, interleaved: bool = False, ws: Optional[torch.Tensor] = None):
+    """Backward of :func:`gdn2_qk_norm_rope_fwd`: dict with dq, dk and, for given weights, dq_weight, dk_weight (fp32;
+    None otherwise)."""
+    with _Device(q) as stream:
+        sizes, lead, tail = _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
+        dev, D = q.device, q.shape[3]
+        g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=k.dtype, device=dev),
+             "dq_weight": None if q_weight is None else torch.empty(D, dtype=torch.float32, device=dev),
+             "dk_weight": None if k_weight is None else torch.empty(D, dtype=torch.float32, device=dev)}
+        if ws is None and (q_weight is not None or k_weight is not None):
+            ws = torch.empty(lib().gdn2_qk_norm_rope_workspace_size(D), dtype=torch.uint8, device=dev)
+        rc = lib().gdn2_qk_norm_rope_bwd(
+            *lead, _opt(dq_out, dev, "dq_out", q.dtype, tuple(q.shape)), _opt(dk_out, dev, "dk_out", q.dtype, tuple(k.shape)),
+            *tail, g["dq"].data_ptr(), g["dk"].data_ptr(),
+            *(None if g[n] is None else g[n].data_ptr() for n in ("dq_weight", "dk_weight")), *sizes,
+            None if ws is None else _on(ws, dev, "ws"), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+    _check("gdn2_qk_norm_rope_bwd", rc)
+    return g
+
+
+class QkNormRope(torch.autograd.Function):
+    """autograd wrapper of the query/key norm and rotation."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved):
+        out = gdn2_qk_norm_rope_fwd(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
+        ctx.save_for_backward(q, k, positions, inv_freq, axes, q_weight, k_weight)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return out
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, positions, inv_freq, axes, q_weight, k_weight = ctx.saved_tensors
+        g = gdn2_qk_norm_rope_bwd(q, k, dq_out.contiguous(), dk_out.contiguous(), positions, inv_freq, axes, q_weight,
+                                  k_weight, ctx.eps, ctx.interleaved)
+        return g["dq"], g["dk"], None, None, None, g["dq_weight"], g["dk_weight"], None, None
+
+
+def qk_norm_rope(q, k, positions, inv_freq, axes=None, q_weight=None, k_weight=None, eps: Optional[float] = 1e-6,
+                 interleaved: bool = False):
+    """Differentiable :func:`gdn2_qk_norm_rope_fwd` (gradients of q, k and the weights). Returns ``(q_out, k_out)``."""
+    return QkNormRope.apply(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
+
+
 def gdn2_device_status(device=None) -> int:
     """Synchronise the current stream and return the device-side status of the tensor-core kernels
     (0, or GDN2_ERR_TIMEOUT if a bounded wait inside them gave up since the previous call; the record is
@@ -421,7 +762,7 @@ def trace_enable(on: bool = True) -> None:
 
 def trace_read() -> dict:
     """{kernel name: (launches, summed device ms)} since the last read (waits for the events)."""
-    n_max = 16
+    n_max = 32
     names = ctypes.create_string_buffer(1024)
     launches = (ctypes.c_int * n_max)()
     ms = (ctypes.c_double * n_max)()

@@ -1,0 +1,337 @@
+// linear_f32.cu -- linear attention with a decay per head in 32-bit precision: forward and backward over whole
+// sequences, in chunks of 64 tokens that run in parallel.
+//
+// Three launches (linear.cuh has the pass they compute):
+//   1. chunk_states_kernel  per chunk, the state its tokens alone leave at its end, sum_j a^{C-1-j} k_j v_j^T (the
+//                           backward also at its start, sum_i a^{i+1} q_i dout_i^T)
+//   2. join_states_kernel   per head, the running state over the chunks: every chunk's start (end) state in place of
+//                           its own contribution, and the final state
+//   3. chunk_out_kernel     per chunk, the outputs: rows of (X Y^T * decay) Z + a^. X R with R the chunk's state
+// The backward's dq, dk and dv are three such passes over two sets of states.
+//
+// The products run on tensor cores with every 32-bit operand split into two tf32 terms, x = big + small (11 + 11
+// significant bits): big big + big small + small big leaves out terms below 2^-22, about what 32-bit rounding of a
+// long sum costs, where plain tf32 operands would leave 2^-11. Sums are 32-bit.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "chunk_common.cuh"
+#include "internal.h"
+#include "linear.cuh"
+
+namespace gdn2 {
+namespace {
+
+using linear::Seqs;
+
+__device__ unsigned int g_linear32_error;
+
+constexpr int C32 = 64;     // tokens of a chunk
+constexpr int NT32 = 256;   // threads of a block
+
+// A 32-bit value as two tf32 terms. An infinity has no remainder.
+__device__ __forceinline__ void split(float x, uint32_t* big, uint32_t* small) {
+    *big = chunk::to_tf32(x);
+    const float b = __uint_as_float(*big);
+    *small = chunk::to_tf32(fabsf(b) < __int_as_float(0x7f800000) ? x - b : 0.f);
+}
+
+// How the 8 warps of a block share an M x N product: WM x WN warps, each MT x NT tiles of 16 x 8.
+template <int M, int N>
+struct WarpTiles {
+    static constexpr int MALL = M / 16, NALL = N / 8;
+    static constexpr int WM = MALL >= 8 ? 4 : MALL >= 2 ? (NALL >= 4 ? 2 : (MALL < 4 ? MALL : 4)) : 1;
+    static constexpr int WN = (8 / WM) < NALL ? 8 / WM : NALL;
+    static constexpr int MT = MALL / WM, NT = NALL / WN;
+    static_assert(MT * WM == MALL && NT * WN == NALL, "tiles must divide");
+};
+
+// acc += A B for this warp's tiles; a(m, k) and b(k, n) give the operands' elements.
+template <int M, int N, int K, typename FA, typename FB>
+__device__ __forceinline__ void warp_gemm(float (&acc)[WarpTiles<M, N>::MT][WarpTiles<M, N>::NT][4], FA a, FB b) {
+    using W = WarpTiles<M, N>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (warp >= W::WM * W::WN) return;
+    const int m0 = (warp / W::WN) * (16 * W::MT), n0 = (warp % W::WN) * (8 * W::NT);
+#pragma unroll 2
+    for (int k0 = 0; k0 < K; k0 += 8) {
+        uint32_t ab[W::MT][4], as[W::MT][4];
+#pragma unroll
+        for (int i = 0; i < W::MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                split(a(m0 + 16 * i + g + 8 * (e & 1), k0 + t + 4 * (e >> 1)), &ab[i][e], &as[i][e]);
+#pragma unroll
+        for (int j = 0; j < W::NT; ++j) {
+            uint32_t bb[2], bs[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) split(b(k0 + t + 4 * e, n0 + 8 * j + g), &bb[e], &bs[e]);
+#pragma unroll
+            for (int i = 0; i < W::MT; ++i) {
+                chunk::mma_tf32_16x8x8(acc[i][j], as[i][0], as[i][1], as[i][2], as[i][3], bb[0], bb[1]);
+                chunk::mma_tf32_16x8x8(acc[i][j], ab[i][0], ab[i][1], ab[i][2], ab[i][3], bs[0], bs[1]);
+                chunk::mma_tf32_16x8x8(acc[i][j], ab[i][0], ab[i][1], ab[i][2], ab[i][3], bb[0], bb[1]);
+            }
+        }
+    }
+}
+
+// Calls f(row, column, acc element) for the elements of this warp's tiles.
+template <int M, int N, typename F>
+__device__ __forceinline__ void each_element(float (&acc)[WarpTiles<M, N>::MT][WarpTiles<M, N>::NT][4], F f) {
+    using W = WarpTiles<M, N>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (warp >= W::WM * W::WN) return;
+    const int m0 = (warp / W::WN) * (16 * W::MT), n0 = (warp % W::WN) * (8 * W::NT);
+#pragma unroll
+    for (int i = 0; i < W::MT; ++i)
+#pragma unroll
+        for (int j = 0; j < W::NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f(m0 + 16 * i + g + 8 * (e >> 1), n0 + 8 * j + 2 * t + (e & 1), acc[i][j][e]);
+}
+
+// One chunk's rows of a token tensor into shared memory as floats, zeros behind the chunk's last token (the rows
+// there may be another sequence's).
+template <int D, int LD>
+__device__ __forceinline__ void load_rows(float* dst, const float* src, long long row0, int valid, int H, int h) {
+    constexpr int PER = D / 4;
+    for (int x = threadIdx.x; x < C32 * PER; x += NT32) {
+        const int r = x / PER, p = x % PER;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < valid) v = *reinterpret_cast<const float4*>(src + ((size_t)(row0 + r) * H + h) * D + 4 * p);
+        *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = v;
+    }
+}
+template <int D, int LD>
+__device__ __forceinline__ void load_rows(float* dst, const __nv_bfloat16* src, long long row0, int valid, int H, int h) {
+    constexpr int PER = D / 4;
+    for (int x = threadIdx.x; x < C32 * PER; x += NT32) {
+        const int r = x / PER, p = x % PER;
+        uint2 u = make_uint2(0, 0);
+        if (r < valid) u = *reinterpret_cast<const uint2*>(src + ((size_t)(row0 + r) * H + h) * D + 4 * p);
+        const float2 lo = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.x));
+        const float2 hi = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.y));
+        *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+}
+
+struct Unit {
+    int n, h, c, len, valid;
+    long long row0, state;   // first token row; index of the chunk's state
+};
+// Blocks are (sequence, head, chunk), chunk fastest. False for a chunk behind its sequence's end.
+__device__ __forceinline__ bool unit_of(const Seqs& s, int nc, Unit* u) {
+    const int x = blockIdx.x;
+    u->c = x % nc;
+    u->h = (x / nc) % s.H;
+    u->n = x / nc / s.H;
+    long long begin;
+    u->len = linear::seq_span(s, u->n, &begin, &g_linear32_error);
+    u->valid = min(C32, u->len - u->c * C32);
+    u->row0 = begin + (long long)u->c * C32;
+    u->state = x;
+    return u->valid > 0;
+}
+
+struct StateJob {
+    const void *y, *z;
+    float* states;       // [N, H, NC, Dk, Dv]
+    const float* start;  // [N, H, Dk, Dv] or null
+    float* end;          // or null
+    int rev;
+};
+struct StateJobs {
+    StateJob job[2];
+};
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, const float* __restrict__ log_decay, StateJobs jobs) {
+    constexpr int LY = DK + 8, LZ = DV + 8;   // 8-column shift a row: the k-major fragment reads meet no bank twice
+    extern __shared__ float sm[];
+    float *Y = sm, *Z = sm + C32 * LY;
+    const StateJob& job = jobs.job[blockIdx.y];
+    Unit u;
+    if (!unit_of(s, nc, &u)) return;
+    const float l2 = linear::log2_decay(log_decay, u.h);
+    load_rows<DK, LY>(Y, static_cast<const Tin*>(job.y), u.row0, u.valid, s.H, u.h);
+    load_rows<DV, LZ>(Z, static_cast<const Tin*>(job.z), u.row0, u.valid, s.H, u.h);
+    __shared__ float f[C32];
+    if (threadIdx.x < C32) {
+        const int j = threadIdx.x;
+        f[j] = j < u.valid ? linear::decay_pow(l2, job.rev ? j + 1 : u.valid - 1 - j) : 0.f;
+    }
+    __syncthreads();
+    float acc[WarpTiles<DK, DV>::MT][WarpTiles<DK, DV>::NT][4] = {};
+    warp_gemm<DK, DV, C32>(acc, [&](int m, int k) { return Y[k * LY + m]; }, [&](int k, int n) { return Z[k * LZ + n] * f[k]; });
+    float* out = job.states + (size_t)u.state * DK * DV;
+    each_element<DK, DV>(acc, [&](int m, int n, float x) { out[m * DV + n] = x; });
+}
+
+// One thread per state element and head: the chunks in order, each contribution replaced by the state in front of it.
+__global__ void __launch_bounds__(256) join_states_kernel(Seqs s, int nc, const float* __restrict__ log_decay, StateJobs jobs) {
+    const StateJob& job = jobs.job[blockIdx.y];
+    const int dd = s.Dk * s.Dv;
+    const int per = dd / 256;
+    const int head = blockIdx.x / per, e = (blockIdx.x % per) * 256 + threadIdx.x;
+    const int n = head / s.H, h = head % s.H;
+    long long begin;
+    const int len = linear::seq_span(s, n, &begin, &g_linear32_error);
+    const float l2 = linear::log2_decay(log_decay, h);
+    const int mine = (len + C32 - 1) / C32;
+    float S = job.start ? job.start[(size_t)head * dd + e] : 0.f;
+    float* st = job.states + (size_t)head * nc * dd + e;
+    const float whole = linear::decay_pow(l2, C32), last = linear::decay_pow(l2, len - (mine - 1) * C32);
+    constexpr int AHEAD = 8;   // loads in flight a thread
+    for (int c0 = 0; c0 < mine; c0 += AHEAD) {
+        float x[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int c = job.rev ? mine - 1 - (c0 + i) : c0 + i;
+            x[i] = c0 + i < mine ? st[(size_t)c * dd] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (c0 + i >= mine) break;
+            const int c = job.rev ? mine - 1 - (c0 + i) : c0 + i;
+            st[(size_t)c * dd] = S;
+            S = fmaf(c == mine - 1 ? last : whole, S, x[i]);
+        }
+    }
+    if (job.end) job.end[(size_t)head * dd + e] = S;
+}
+
+struct OutJob {
+    const void *x, *y, *z;
+    const float* states;
+    void* out;
+    int rev, transposed;   // transposed: the state is read as [DZ][DR]
+};
+struct OutJobs {
+    OutJob job[2];
+};
+
+template <typename Tin, int DR, int DZ>
+__global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const float* __restrict__ log_decay, OutJobs jobs) {
+    constexpr int LX = DR + 4, LZ = DZ + 8, LP = C32 + 4;
+    extern __shared__ float sm[];
+    float *X = sm, *Y = X + C32 * LX, *Z = Y + C32 * LX, *P = Z + C32 * LZ;
+    __shared__ float pw[C32 + 1];
+    const OutJob& job = jobs.job[blockIdx.y];
+    Unit u;
+    if (!unit_of(s, nc, &u)) return;
+    const float l2 = linear::log2_decay(log_decay, u.h);
+    load_rows<DR, LX>(X, static_cast<const Tin*>(job.x), u.row0, u.valid, s.H, u.h);
+    load_rows<DR, LX>(Y, static_cast<const Tin*>(job.y), u.row0, u.valid, s.H, u.h);
+    load_rows<DZ, LZ>(Z, static_cast<const Tin*>(job.z), u.row0, u.valid, s.H, u.h);
+    if (threadIdx.x <= C32) pw[threadIdx.x] = linear::decay_pow(l2, threadIdx.x);
+    __syncthreads();
+    {
+        float p[WarpTiles<C32, C32>::MT][WarpTiles<C32, C32>::NT][4] = {};
+        warp_gemm<C32, C32, DR>(p, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return Y[n * LX + k]; });
+        each_element<C32, C32>(p, [&](int m, int n, float x) {
+            const int far = job.rev ? n - m : m - n;
+            P[m * LP + n] = far >= 0 ? x * pw[far] : 0.f;
+        });
+    }
+    float acc[WarpTiles<C32, DZ>::MT][WarpTiles<C32, DZ>::NT][4] = {};
+    const float* S = job.states + (size_t)u.state * DR * DZ;
+    if (job.transposed)
+        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return __ldg(S + n * DR + k); });
+    else
+        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return __ldg(S + k * DZ + n); });
+    each_element<C32, DZ>(acc, [&](int m, int, float& x) { x *= m < u.valid ? pw[job.rev ? u.valid - 1 - m : m + 1] : 0.f; });
+    __syncthreads();
+    warp_gemm<C32, DZ, C32>(acc, [&](int m, int k) { return P[m * LP + k]; }, [&](int k, int n) { return Z[k * LZ + n]; });
+    Tin* out = static_cast<Tin*>(job.out);
+    each_element<C32, DZ>(acc, [&](int m, int n, float x) {
+        if (m < u.valid) out[((size_t)(u.row0 + m) * s.H + u.h) * DZ + n] = from_f32<Tin>(x);
+    });
+}
+
+int chunks_of(const Seqs& s) { return (s.T + C32 - 1) / C32; }
+
+template <typename Tin, int DK, int DV>
+cudaError_t states(const LinearArgs& a, int nc, const StateJobs& jobs, int n, cudaStream_t s) {
+    const int smem = (int)sizeof(float) * C32 * (DK + 8 + DV + 8);
+    cudaError_t e = cudaFuncSetAttribute(chunk_states_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    TraceScope trace(K_LINEAR_STATES, s);
+    chunk_states_kernel<Tin, DK, DV><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    return cudaGetLastError();
+}
+template <typename Tin, int DR, int DZ>
+cudaError_t outputs(const LinearArgs& a, int nc, const OutJobs& jobs, int n, cudaStream_t s) {
+    const int smem = (int)sizeof(float) * C32 * (2 * (DR + 4) + DZ + 8 + C32 + 4);
+    cudaError_t e = cudaFuncSetAttribute(chunk_out_kernel<Tin, DR, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    TraceScope trace(K_LINEAR_OUT, s);
+    chunk_out_kernel<Tin, DR, DZ><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    return cudaGetLastError();
+}
+
+template <typename Tin, int DK, int DV>
+cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
+    const int nc = chunks_of(a.seq);
+    const size_t set = (size_t)a.seq.N * a.seq.H * nc * DK * DV;
+    float* w = static_cast<float*>(a.ws);
+    StateJobs sj{};
+    int n = 0;
+    sj.job[n++] = StateJob{a.k, a.v, w, a.S0, bwd ? nullptr : a.ST, 0};
+    if (bwd) sj.job[n++] = StateJob{a.q, a.dout, w + set, a.dST, a.dS0, 1};
+    cudaError_t e = nc ? states<Tin, DK, DV>(a, nc, sj, n, s) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    {
+        TraceScope trace(K_LINEAR_JOIN, s);
+        join_states_kernel<<<dim3(a.seq.N * a.seq.H * (DK * DV / 256), n), 256, 0, s>>>(a.seq, nc, a.log_decay, sj);
+        if ((e = cudaGetLastError()) != cudaSuccess || !nc) return e;
+    }
+    OutJobs oj{};
+    if (!bwd) {
+        oj.job[0] = OutJob{a.q, a.k, a.v, w, a.o, 0, 0};
+        return outputs<Tin, DK, DV>(a, nc, oj, 1, s);
+    }
+    oj.job[0] = OutJob{a.dout, a.v, a.k, w, a.dq, 0, 1};
+    oj.job[1] = OutJob{a.v, a.dout, a.q, w + set, a.dk, 1, 1};
+    if ((e = outputs<Tin, DV, DK>(a, nc, oj, 2, s)) != cudaSuccess) return e;
+    oj.job[0] = OutJob{a.k, a.q, a.dout, w + set, a.dv, 1, 0};
+    return outputs<Tin, DK, DV>(a, nc, oj, 1, s);
+}
+
+template <typename Tin, int DK>
+cudaError_t run_dv(const LinearArgs& a, bool bwd, cudaStream_t s) {
+    switch (a.seq.Dv) {
+    case 16: return run<Tin, DK, 16>(a, bwd, s);
+    case 32: return run<Tin, DK, 32>(a, bwd, s);
+    case 64: return run<Tin, DK, 64>(a, bwd, s);
+    default: return run<Tin, DK, 128>(a, bwd, s);
+    }
+}
+template <typename Tin>
+cudaError_t run_dk(const LinearArgs& a, bool bwd, cudaStream_t s) {
+    switch (a.seq.Dk) {
+    case 16: return run_dv<Tin, 16>(a, bwd, s);
+    case 32: return run_dv<Tin, 32>(a, bwd, s);
+    case 64: return run_dv<Tin, 64>(a, bwd, s);
+    default: return run_dv<Tin, 128>(a, bwd, s);
+    }
+}
+
+}  // namespace
+
+size_t linear32_workspace(const Seqs& s, bool backward) {
+    return (size_t)s.N * s.H * chunks_of(s) * s.Dk * s.Dv * sizeof(float) * (backward ? 2 : 1);
+}
+
+cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
+    return a.dt == GDN2_BF16 ? run_dk<__nv_bfloat16>(a, bwd, s) : run_dk<float>(a, bwd, s);
+}
+
+cudaError_t linear32_take_errors(unsigned int* bits) {
+    cudaError_t e = cudaMemcpyFromSymbol(bits, g_linear32_error, sizeof(unsigned int));
+    if (e != cudaSuccess) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_linear32_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace gdn2

@@ -22,7 +22,9 @@ namespace {
 const char* kNames[KERNEL_COUNT] = {"chunk_fwd_kernel", "chunk_bwd_kernel", "recurrent_fwd_kernel",
                                     "recurrent_bwd_kernel", "decode_kernel", "gate_expand_kernel",
                                     "gate_reduce_kernel", "pad_copy_kernel", "split_prefix_kernel",
-                                    "state_affine_kernel", "gates_fwd_kernel", "gates_bwd_kernel"};
+                                    "state_affine_kernel", "gates_fwd_kernel", "gates_bwd_kernel",
+                                    "chunk_states_kernel", "join_states_kernel", "chunk_out_kernel",
+                                    "linear_step_kernel", "qk_rope_fwd_kernel", "qk_rope_bwd_kernel"};
 
 std::atomic<int> g_on{0};
 std::mutex g_mu;
