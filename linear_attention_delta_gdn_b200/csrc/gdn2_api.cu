@@ -165,16 +165,19 @@ gdn2_status gdn2_device_status(void* stream) {
     if ((e = chunk_bwd_take_errors(&bwd)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (backward record)");
     unsigned int vl = 0;
     if ((e = varlen_take_errors(&vl)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (varlen record)");
-    unsigned int lin = 0, step = 0, rope = 0;
-    if ((e = linear32_take_errors(&lin)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
+    unsigned int lin = 0, lin32 = 0, step = 0, rope = 0;
+    if ((e = linear_chunk_take_errors(&lin)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
+    if ((e = linear32_take_errors(&lin32)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
     if ((e = linear_step_take_errors(&step)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (step record)");
     if ((e = qk_rope_take_errors(&rope)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (rotation record)");
     if (vl)
         return fail(GDN2_ERR_INVALID, "cu_seqlens: %s%s", (vl & 1u) ? "a sequence was longer than Tmax (cut) " : "",
                     (vl & 2u) ? "a sequence lay outside [0, Ttot) or had a negative length (dropped)" : "");
+    lin |= lin32;
     if (lin & (linear::ERR_LONG | linear::ERR_OUTSIDE))
         return fail(GDN2_ERR_INVALID, "cu_seqlens: %s%s", (lin & linear::ERR_LONG) ? "a sequence was longer than Tmax (cut) " : "",
                     (lin & linear::ERR_OUTSIDE) ? "a sequence lay outside [0, Ttot) or had a negative length (dropped)" : "");
+    if (lin & linear::ERR_WAIT) return fail(GDN2_ERR_TIMEOUT, "device wait gave up: linear_chunk_kernel");
     if (step & linear::ERR_SLOT)
         return fail(GDN2_ERR_INVALID, "slots: a row's slot lay outside the pool, or an earlier row had named it (row skipped)");
     if (rope) return fail(GDN2_ERR_INVALID, "axes: a pair's axis lay outside [0, num_axes) (pair not turned)");

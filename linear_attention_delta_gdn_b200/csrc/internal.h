@@ -120,7 +120,7 @@ cudaError_t gates_bwd_launch(const void* z, const void* dq, const void* dk, cons
 // Kernels of the library, for gdn2_trace_read().
 enum KernelId { K_CHUNK_FWD = 0, K_CHUNK_BWD, K_REC_FWD, K_REC_BWD, K_DECODE, K_GATE_EXPAND, K_GATE_REDUCE,
                 K_VARLEN_COPY, K_SPLIT_PREFIX, K_STATE_AFFINE, K_LAYER_GATES, K_LAYER_GATES_BWD,
-                K_LINEAR_STATES, K_LINEAR_JOIN, K_LINEAR_OUT, K_LINEAR_STEP, K_QK_ROPE, K_QK_ROPE_BWD, KERNEL_COUNT };
+                K_LINEAR_CHUNK, K_LINEAR_SEGMENT, K_LINEAR_STATES, K_LINEAR_JOIN, K_LINEAR_OUT, K_LINEAR_STEP, K_QK_ROPE, K_QK_ROPE_BWD, KERNEL_COUNT };
 
 // Brackets one kernel launch with CUDA events on its stream while tracing is on.
 class TraceScope {

@@ -74,9 +74,15 @@ struct LinearArgs {
     float *ST, *dS0;
     void* ws;
 };
+// fp32 (linear_f32.cu)
 size_t linear32_workspace(const linear::Seqs& s, bool backward);
 cudaError_t linear32_launch(const LinearArgs& a, bool backward, cudaStream_t s);
 cudaError_t linear32_take_errors(unsigned int* bits);
+
+// bf16 on tensor cores (linear_chunk.cu)
+size_t linear_chunk_workspace(const linear::Seqs& s, bool backward);
+cudaError_t linear_chunk_launch(const LinearArgs& a, bool backward, cudaStream_t s);
+cudaError_t linear_chunk_take_errors(unsigned int* bits);
 
 struct LinearStepArgs {
     gdn2_dtype dt;

@@ -70,8 +70,7 @@ gdn2_status check_dims(const linear::Seqs& s, gdn2_dtype dt) {
     } while (0)
 
 size_t workspace(const linear::Seqs& s, gdn2_dtype dt, bool bwd) {
-    (void)dt;
-    return align256(linear32_workspace(s, bwd));
+    return align256(dt == GDN2_BF16 ? linear_chunk_workspace(s, bwd) : linear32_workspace(s, bwd));
 }
 
 gdn2_status run(const linear::Seqs& seq, const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
@@ -105,7 +104,8 @@ gdn2_status run(const linear::Seqs& seq, const void* q, const void* k, const voi
     a.log_decay = log_decay; a.S0 = S0; a.dST = dST;
     a.o = o; a.ST = ST; a.dq = dq; a.dk = dk; a.dv = dv; a.dS0 = dS0;
     a.ws = ws;
-    return cuda_status(linear32_launch(a, bwd, static_cast<cudaStream_t>(stream)), fn);
+    cudaStream_t str = static_cast<cudaStream_t>(stream);
+    return cuda_status(dt == GDN2_BF16 ? linear_chunk_launch(a, bwd, str) : linear32_launch(a, bwd, str), fn);
 }
 
 linear::Seqs dense(int B, int T, int H, int Dk, int Dv) {

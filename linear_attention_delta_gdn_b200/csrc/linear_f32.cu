@@ -12,7 +12,6 @@
 // The products run on tensor cores with every 32-bit operand split into two tf32 terms, x = big + small (11 + 11
 // significant bits): big big + big small + small big leaves out terms below 2^-22, about what 32-bit rounding of a
 // long sum costs, where plain tf32 operands would leave 2^-11. Sums are 32-bit.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"
@@ -103,19 +102,6 @@ __device__ __forceinline__ void load_rows(float* dst, const float* src, long lon
         *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = v;
     }
 }
-template <int D, int LD>
-__device__ __forceinline__ void load_rows(float* dst, const __nv_bfloat16* src, long long row0, int valid, int H, int h) {
-    constexpr int PER = D / 4;
-    for (int x = threadIdx.x; x < C32 * PER; x += NT32) {
-        const int r = x / PER, p = x % PER;
-        uint2 u = make_uint2(0, 0);
-        if (r < valid) u = *reinterpret_cast<const uint2*>(src + ((size_t)(row0 + r) * H + h) * D + 4 * p);
-        const float2 lo = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.x));
-        const float2 hi = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&u.y));
-        *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = make_float4(lo.x, lo.y, hi.x, hi.y);
-    }
-}
-
 struct Unit {
     int n, h, c, len, valid;
     long long row0, state;   // first token row; index of the chunk's state
@@ -145,7 +131,7 @@ struct StateJobs {
     StateJob job[2];
 };
 
-template <typename Tin, int DK, int DV>
+template <int DK, int DV>
 __global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, const float* __restrict__ log_decay, StateJobs jobs) {
     constexpr int LY = DK + 8, LZ = DV + 8;   // 8-column shift a row: the k-major fragment reads meet no bank twice
     extern __shared__ float sm[];
@@ -154,8 +140,8 @@ __global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, cons
     Unit u;
     if (!unit_of(s, nc, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
-    load_rows<DK, LY>(Y, static_cast<const Tin*>(job.y), u.row0, u.valid, s.H, u.h);
-    load_rows<DV, LZ>(Z, static_cast<const Tin*>(job.z), u.row0, u.valid, s.H, u.h);
+    load_rows<DK, LY>(Y, static_cast<const float*>(job.y), u.row0, u.valid, s.H, u.h);
+    load_rows<DV, LZ>(Z, static_cast<const float*>(job.z), u.row0, u.valid, s.H, u.h);
     __shared__ float f[C32];
     if (threadIdx.x < C32) {
         const int j = threadIdx.x;
@@ -211,7 +197,7 @@ struct OutJobs {
     OutJob job[2];
 };
 
-template <typename Tin, int DR, int DZ>
+template <int DR, int DZ>
 __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const float* __restrict__ log_decay, OutJobs jobs) {
     constexpr int LX = DR + 4, LZ = DZ + 8, LP = C32 + 4;
     extern __shared__ float sm[];
@@ -221,9 +207,9 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const f
     Unit u;
     if (!unit_of(s, nc, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
-    load_rows<DR, LX>(X, static_cast<const Tin*>(job.x), u.row0, u.valid, s.H, u.h);
-    load_rows<DR, LX>(Y, static_cast<const Tin*>(job.y), u.row0, u.valid, s.H, u.h);
-    load_rows<DZ, LZ>(Z, static_cast<const Tin*>(job.z), u.row0, u.valid, s.H, u.h);
+    load_rows<DR, LX>(X, static_cast<const float*>(job.x), u.row0, u.valid, s.H, u.h);
+    load_rows<DR, LX>(Y, static_cast<const float*>(job.y), u.row0, u.valid, s.H, u.h);
+    load_rows<DZ, LZ>(Z, static_cast<const float*>(job.z), u.row0, u.valid, s.H, u.h);
     if (threadIdx.x <= C32) pw[threadIdx.x] = linear::decay_pow(l2, threadIdx.x);
     __syncthreads();
     {
@@ -243,34 +229,34 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const f
     each_element<C32, DZ>(acc, [&](int m, int, float& x) { x *= m < u.valid ? pw[job.rev ? u.valid - 1 - m : m + 1] : 0.f; });
     __syncthreads();
     warp_gemm<C32, DZ, C32>(acc, [&](int m, int k) { return P[m * LP + k]; }, [&](int k, int n) { return Z[k * LZ + n]; });
-    Tin* out = static_cast<Tin*>(job.out);
+    float* out = static_cast<float*>(job.out);
     each_element<C32, DZ>(acc, [&](int m, int n, float x) {
-        if (m < u.valid) out[((size_t)(u.row0 + m) * s.H + u.h) * DZ + n] = from_f32<Tin>(x);
+        if (m < u.valid) out[((size_t)(u.row0 + m) * s.H + u.h) * DZ + n] = x;
     });
 }
 
 int chunks_of(const Seqs& s) { return (s.T + C32 - 1) / C32; }
 
-template <typename Tin, int DK, int DV>
+template <int DK, int DV>
 cudaError_t states(const LinearArgs& a, int nc, const StateJobs& jobs, int n, cudaStream_t s) {
     const int smem = (int)sizeof(float) * C32 * (DK + 8 + DV + 8);
-    cudaError_t e = cudaFuncSetAttribute(chunk_states_kernel<Tin, DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_states_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TraceScope trace(K_LINEAR_STATES, s);
-    chunk_states_kernel<Tin, DK, DV><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    chunk_states_kernel<DK, DV><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
     return cudaGetLastError();
 }
-template <typename Tin, int DR, int DZ>
+template <int DR, int DZ>
 cudaError_t outputs(const LinearArgs& a, int nc, const OutJobs& jobs, int n, cudaStream_t s) {
     const int smem = (int)sizeof(float) * C32 * (2 * (DR + 4) + DZ + 8 + C32 + 4);
-    cudaError_t e = cudaFuncSetAttribute(chunk_out_kernel<Tin, DR, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(chunk_out_kernel<DR, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TraceScope trace(K_LINEAR_OUT, s);
-    chunk_out_kernel<Tin, DR, DZ><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    chunk_out_kernel<DR, DZ><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
     return cudaGetLastError();
 }
 
-template <typename Tin, int DK, int DV>
+template <int DK, int DV>
 cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
     const int nc = chunks_of(a.seq);
     const size_t set = (size_t)a.seq.N * a.seq.H * nc * DK * DV;
@@ -279,7 +265,7 @@ cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
     int n = 0;
     sj.job[n++] = StateJob{a.k, a.v, w, a.S0, bwd ? nullptr : a.ST, 0};
     if (bwd) sj.job[n++] = StateJob{a.q, a.dout, w + set, a.dST, a.dS0, 1};
-    cudaError_t e = nc ? states<Tin, DK, DV>(a, nc, sj, n, s) : cudaSuccess;
+    cudaError_t e = nc ? states<DK, DV>(a, nc, sj, n, s) : cudaSuccess;
     if (e != cudaSuccess) return e;
     {
         TraceScope trace(K_LINEAR_JOIN, s);
@@ -289,31 +275,30 @@ cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
     OutJobs oj{};
     if (!bwd) {
         oj.job[0] = OutJob{a.q, a.k, a.v, w, a.o, 0, 0};
-        return outputs<Tin, DK, DV>(a, nc, oj, 1, s);
+        return outputs<DK, DV>(a, nc, oj, 1, s);
     }
     oj.job[0] = OutJob{a.dout, a.v, a.k, w, a.dq, 0, 1};
     oj.job[1] = OutJob{a.v, a.dout, a.q, w + set, a.dk, 1, 1};
-    if ((e = outputs<Tin, DV, DK>(a, nc, oj, 2, s)) != cudaSuccess) return e;
+    if ((e = outputs<DV, DK>(a, nc, oj, 2, s)) != cudaSuccess) return e;
     oj.job[0] = OutJob{a.k, a.q, a.dout, w + set, a.dv, 1, 0};
-    return outputs<Tin, DK, DV>(a, nc, oj, 1, s);
+    return outputs<DK, DV>(a, nc, oj, 1, s);
 }
 
-template <typename Tin, int DK>
+template <int DK>
 cudaError_t run_dv(const LinearArgs& a, bool bwd, cudaStream_t s) {
     switch (a.seq.Dv) {
-    case 16: return run<Tin, DK, 16>(a, bwd, s);
-    case 32: return run<Tin, DK, 32>(a, bwd, s);
-    case 64: return run<Tin, DK, 64>(a, bwd, s);
-    default: return run<Tin, DK, 128>(a, bwd, s);
+    case 16: return run<DK, 16>(a, bwd, s);
+    case 32: return run<DK, 32>(a, bwd, s);
+    case 64: return run<DK, 64>(a, bwd, s);
+    default: return run<DK, 128>(a, bwd, s);
     }
 }
-template <typename Tin>
 cudaError_t run_dk(const LinearArgs& a, bool bwd, cudaStream_t s) {
     switch (a.seq.Dk) {
-    case 16: return run_dv<Tin, 16>(a, bwd, s);
-    case 32: return run_dv<Tin, 32>(a, bwd, s);
-    case 64: return run_dv<Tin, 64>(a, bwd, s);
-    default: return run_dv<Tin, 128>(a, bwd, s);
+    case 16: return run_dv<16>(a, bwd, s);
+    case 32: return run_dv<32>(a, bwd, s);
+    case 64: return run_dv<64>(a, bwd, s);
+    default: return run_dv<128>(a, bwd, s);
     }
 }
 
@@ -324,7 +309,7 @@ size_t linear32_workspace(const Seqs& s, bool backward) {
 }
 
 cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
-    return a.dt == GDN2_BF16 ? run_dk<__nv_bfloat16>(a, bwd, s) : run_dk<float>(a, bwd, s);
+    return run_dk(a, bwd, s);
 }
 
 cudaError_t linear32_take_errors(unsigned int* bits) {

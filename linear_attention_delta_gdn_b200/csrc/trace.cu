@@ -23,6 +23,7 @@ const char* kNames[KERNEL_COUNT] = {"chunk_fwd_kernel", "chunk_bwd_kernel", "rec
                                     "recurrent_bwd_kernel", "decode_kernel", "gate_expand_kernel",
                                     "gate_reduce_kernel", "pad_copy_kernel", "split_prefix_kernel",
                                     "state_affine_kernel", "gates_fwd_kernel", "gates_bwd_kernel",
+                                    "linear_chunk_kernel", "linear_segment_kernel",
                                     "chunk_states_kernel", "join_states_kernel", "chunk_out_kernel",
                                     "linear_step_kernel", "qk_rope_fwd_kernel", "qk_rope_bwd_kernel"};
 
