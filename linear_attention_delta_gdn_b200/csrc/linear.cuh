@@ -43,12 +43,12 @@ __device__ __forceinline__ int seq_span(const Seqs& s, int n, long long* begin, 
     const int b = s.cu[n], e = s.cu[n + 1];
     *begin = b;
     if (b < 0 || e < b || e > s.Ttot) {
-        if (threadIdx.x == 0) atomicOr(err, ERR_OUTSIDE);
+        if ((threadIdx.x & 31) == 0) atomicOr(err, ERR_OUTSIDE);
         *begin = 0;
         return 0;
     }
     if (e - b > s.T) {
-        if (threadIdx.x == 0) atomicOr(err, ERR_LONG);
+        if ((threadIdx.x & 31) == 0) atomicOr(err, ERR_LONG);
         return s.T;
     }
     return e - b;

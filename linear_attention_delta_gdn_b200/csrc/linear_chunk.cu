@@ -5,7 +5,7 @@
 //     out = diag(f) X R + P Z,        R' = a^C R + Y^T diag(g) Z
 // A block owns 64 columns of Z (and of out and R), so a head of 128 is two blocks and 64 heads fill the GPU; X and Y
 // are then read by both, the second time from L2. Products per chunk and block (tcgen05, M = 128, 32-bit TMEM):
-//     A = X Y^T (N 128)    D = Y^T Zh + Y^T Zl (N 64)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
+//     A = X Y^T (N 128)    D = Y^T [Zh | Zl] (N 128)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
@@ -60,7 +60,7 @@ struct Params {
     const float* log_decay;
     int npass, dr, dz, slices;
     int nseg, cps;           // segments of a sequence at most, chunks of a segment
-    long long items;
+    int items;
 };
 
 // One work item and the chunk range it walks.
@@ -74,24 +74,33 @@ struct Item {
     __device__ __forceinline__ int valid(int c) const { return min(CT, len - c * CT); }
     __device__ __forceinline__ int count() const { return c1 - c0; }
 };
+// Once an item and by every role: a function, for the instruction cache's sake.
 template <bool STATES>
-__device__ __forceinline__ Item item_of(const Params& p, long long x) {
-    Item t;
-    t.slice = (int)(x % p.slices); x /= p.slices;
-    t.pass = (int)(x % p.npass); x /= p.npass;
-    t.h = (int)(x % p.seq.H); x /= p.seq.H;
-    t.n = (int)(x % p.seq.N);
-    t.seg = (int)(x / p.seq.N);
-    t.p = &p.pass[t.pass];
-    t.len = linear::seq_span(p.seq, t.n, &t.row0, &g_linear_error);
-    t.nc = (t.len + CT - 1) / CT;
-    t.c0 = min(t.nc, t.seg * p.cps);
-    t.c1 = min(t.nc, t.c0 + p.cps);
+__device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
+    const uint32_t slices = p.slices, npass = p.npass, H = p.seq.H, N = p.seq.N;
+    t->slice = x % slices;
+    x /= slices;
+    t->pass = x % npass;
+    x /= npass;
+    t->h = x % H;
+    x /= H;
+    t->n = x % N;
+    t->seg = x / N;
+    t->p = &p.pass[t->pass];
+    t->len = linear::seq_span(p.seq, t->n, &t->row0, &g_linear_error);
+    t->nc = (t->len + CT - 1) / CT;
+    t->c0 = (int)min((long long)t->nc, (long long)t->seg * p.cps);
+    t->c1 = min(t->nc, t->c0 + p.cps);
     if (STATES) {   // nothing comes behind the last segment (in front of the first one, backwards)
-        const int last = (t.nc + p.cps - 1) / p.cps - 1;
-        if (t.p->rev ? t.seg == 0 : t.seg >= last) t.c1 = t.c0;
+        const int last = (t->nc + p.cps - 1) / p.cps - 1;
+        if (t->p->rev ? t->seg == 0 : t->seg >= last) t->c1 = t->c0;
     }
-    t.l2 = linear::log2_decay(p.log_decay, t.h);
+    t->l2 = linear::log2_decay(p.log_decay, t->h);
+}
+template <bool STATES>
+__device__ __forceinline__ Item item_of(const Params& p, int x) {
+    Item t;
+    find_item<STATES>(p, (uint32_t)x, &t);
     return t;
 }
 
@@ -106,20 +115,78 @@ struct Cfg {
     static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + STAGES * ZB,
                               OFF_ZL = OFF_ZH + ZB, OFF_S = OFF_ZL + ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
     static constexpr uint32_t SMEM = TOTAL + 1024;                 // tiles start on 1024 bytes
-    // TMEM columns: A (then P in its first half) twice, D twice, O1, O2
+    // TMEM columns: A (then P in its first half) twice, D (its Zh and its Zl part), O1, O2
     static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 384, T_O2 = 448;
 };
 
 struct Bars {
     uint64_t full_x[3], full_y[3], full_z[3], empty_x[3], empty_y[3], empty_z[3];
-    uint64_t a_full[2], a_free[2], p_full, z_full, d_full[2], d_free[2], s_full, s_free, o_full, o_free, drain;
+    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full, o_free, drain;
 };
 
-// Waits by a whole warp: every lane has the same answer.
+// The chunk loops of five kinds of warps share one instruction cache, and a loop that runs through it straight costs
+// more in fetches than in work: the loops below are kept short (rolled over column blocks), and what a wait does when
+// its barrier is not there yet is one function for all of them. It reads the timer every 16 tries (a try sleeps a while).
+constexpr uint32_t TRY_NS = 20000;   // how long a try may sleep
+__device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t phase) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(addr), "r"(phase), "r"(TRY_NS)
+        : "memory");
+    return done != 0;
+}
+__device__ __noinline__ bool wait_on(uint32_t addr, uint32_t phase) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
+        if (try_wait(addr, phase)) return true;
+        if ((tries & 15) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > 2000000000ull) return false;
+        }
+    }
+}
+// One thread.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase) {
+    const uint32_t addr = smem_u32(bar);
+    return try_wait(addr, phase) || wait_on(addr, phase);
+}
+// A whole warp: one lane asks (a dozen warps asking with every lane get in each other's way), all have its answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase));
-    if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
-    return ok;
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        ok = wait(bar, phase);
+        if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
+    }
+    return __shfl_sync(0xffffffffu, ok, 0);
+}
+
+// Two 32-bit operations in one issue slot (the rate is that of single ones; slots are what the warps compete for).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
 }
 
 // ------------------------------------------------------------ warp 0: loads
@@ -129,26 +196,26 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
     uint32_t ny = 0, nx = 0, nz = 0;   // tiles asked for so far, over all items
     bool ok = true;
-    for (long long it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
         const Item t = item_of<STATES>(p, it);
         for (int i = 0; i < t.count(); ++i) {
             const uint32_t s = ny % K::STAGES, ph = ((ny / K::STAGES) & 1) ^ 1;
             const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
-            if (!(ok = mbar_wait(&b.empty_y[s], ph))) break;
+            if (!(ok = wait(&b.empty_y[s], ph))) break;
             mbar_arrive_expect_tx(&b.full_y[s], K::YB);
 #pragma unroll
             for (int c = 0; c < DRP / 64; ++c)
                 tma_load_3d(sm + K::OFF_Y + s * K::YB + c * CT * 128, &t.p->y, 64 * c, t.h, row, &b.full_y[s]);
             ++ny;
             if (!STATES) {
-                if (!(ok = mbar_wait(&b.empty_x[s], ph))) break;
+                if (!(ok = wait(&b.empty_x[s], ph))) break;
                 mbar_arrive_expect_tx(&b.full_x[s], K::XB);
 #pragma unroll
                 for (int c = 0; c < DRP / 64; ++c)
                     tma_load_3d(sm + s * K::XB + c * CT * 128, &t.p->x, 64 * c, t.h, row, &b.full_x[s]);
                 ++nx;
             }
-            if (!(ok = mbar_wait(&b.empty_z[s], ph))) break;
+            if (!(ok = wait(&b.empty_z[s], ph))) break;
             mbar_arrive_expect_tx(&b.full_z[s], K::ZB);
             tma_load_3d(sm + K::OFF_Z + s * K::ZB, &t.p->z, t.slice * SL, t.h, row, &b.full_z[s]);
             ++nz;
@@ -159,7 +226,7 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     // let the copies in flight land before the block gives up its shared memory: each stage's last one
     auto land = [](uint64_t* full, uint32_t asked) {
         for (uint32_t k = 1; k <= (uint32_t)K::STAGES && k <= asked; ++k)
-            mbar_wait(&full[(asked - k) % K::STAGES], ((asked - k) / K::STAGES) & 1);
+            wait(&full[(asked - k) % K::STAGES], ((asked - k) / K::STAGES) & 1);
     };
     land(b.full_y, ny);
     land(b.full_x, nx);
@@ -171,131 +238,193 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
 template <int DRP, bool STATES>
 __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, Bars& b) {
     using K = Cfg<DRP, STATES>;
+    // Descriptors of the tiles' first K step: a stage or a K step adds its byte offset / 16 to the address field.
+    // Making them anew for every product costs more time than the product takes.
     const uint32_t base = smem_u32(sm);
-    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, SL, true, true),
+    const uint64_t x_k = desc_k(base, CT, 0, 0), y_k = desc_k(base + K::OFF_Y, CT, 0, 0),
+                   y_mn = desc_mn(base + K::OFF_Y, CT, 0, 0), z_mn = desc_mn(base + K::OFF_Z, CT, 0, 0),
+                   zh_mn = desc_mn(base + K::OFF_ZH, CT, 0, 0), s_mn = desc_mn(base + K::OFF_S, DRP, 0, 0);
+    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, 2 * SL, true, true),
                    idO = idesc_bf16(128, SL, false, true);
-    const int kr = p.dr / 16;   // K steps over the row operand's real channels
-    uint32_t n = 0;
-    bool ok = true;
-    for (long long x = blockIdx.x; ok && x < p.items; x += gridDim.x) {
-        const Item t = item_of<STATES>(p, x);
-        for (int i = 0; i < t.count(); ++i, ++n) {
-            const uint32_t s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, dph = (n >> 1) & 1, one = n & 1;
-            const uint32_t xt = base + s * K::XB, yt = base + K::OFF_Y + s * K::YB, zt = base + K::OFF_Z + s * K::ZB;
-            const bool ragged = t.valid(t.chunk(i)) < CT;
-            if (!(ok = mbar_wait(&b.full_y[s], ph))) break;
-            // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
-            if (ragged && !(ok = mbar_wait(&b.z_full, one))) break;
-            if (!STATES) {
-                if (!(ok = mbar_wait(&b.full_x[s], ph) && mbar_wait(&b.a_free[d], dph ^ 1))) break;
-                tc_fence_after();
-                for (int kk = 0; kk < kr; ++kk)
-                    mma_bf16(tm + K::T_A + d * CT, desc_k(xt, CT, 0, kk), desc_k(yt, CT, 0, kk), idA, kk > 0);
-                mma_commit(&b.a_full[d]);
-            }
-            if (!(ok = mbar_wait(&b.z_full, one) && mbar_wait(&b.d_free[d], dph ^ 1))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < CT / 16; ++kk)
-                mma_bf16(tm + K::T_D + d * SL, desc_mn(yt, CT, 0, kk), desc_mn(base + K::OFF_ZH, CT, 0, kk), idD, kk > 0);
-#pragma unroll
-            for (int kk = 0; kk < CT / 16; ++kk)
-                mma_bf16(tm + K::T_D + d * SL, desc_mn(yt, CT, 0, kk), desc_mn(base + K::OFF_ZL, CT, 0, kk), idD, 1);
-            mma_commit(&b.d_full[d]);
-            mma_commit(&b.empty_y[s]);
-            if (STATES) {
-                mma_commit(&b.empty_z[s]);
-                continue;
-            }
-            if (!(ok = mbar_wait(&b.s_full, one) && mbar_wait(&b.o_free, one ^ 1))) break;
-            tc_fence_after();
-            for (int kk = 0; kk < kr; ++kk)
-                mma_bf16(tm + K::T_O1, desc_k(xt, CT, 0, kk), desc_mn(base + K::OFF_S, DRP, 0, kk), idO, kk > 0);
-            mma_commit(&b.s_free);
-            mma_commit(&b.empty_x[s]);
-            if (!(ok = mbar_wait(&b.full_z[s], ph) && mbar_wait(&b.p_full, one))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < CT / 16; ++kk)
-                mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, desc_mn(zt, CT, 0, kk), idO, kk > 0);
-            mma_commit(&b.o_full);
-            mma_commit(&b.a_free[d]);
-            mma_commit(&b.empty_z[s]);
+    constexpr uint64_t MN = (16 * 128) >> 4;   // 16 rows of an MN-major tile
+    // K-major: 32 bytes a step within a panel of 64 columns, then the next panel
+    auto k_step = [](int kk) { return (uint64_t)(((kk >> 2) * CT * 128 + (kk & 3) * 32) >> 4); };
+    // Two cursors over the same chunks. A of the next chunk is issued before O1 and O2 of this one, so that turning it
+    // into P has the time of all the products in between.
+    struct Cursor {
+        int x, i, count;
+        bool ragged_end;   // the item's chunk range ends in a partial chunk
+        bool rev;
+        uint32_t n;
+    };
+    auto settle = [&](Cursor& c) {   // to the cursor's chunk, into the next items if need be; false behind the last
+        while (c.i >= c.count) {
+            if (c.count >= 0) c.x += gridDim.x;
+            if (c.x >= p.items) return false;
+            const Item t = item_of<STATES>(p, c.x);
+            c.i = 0;
+            c.count = t.count();
+            c.rev = t.p->rev;
+            c.ragged_end = c.count > 0 && t.valid(t.c1 - 1) < CT;
         }
+        return true;
+    };
+    bool ok = true;
+    auto issue_pairs = [&](Cursor& c) {   // A of the cursor's chunk; moves on
+        const uint32_t n = c.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, dph = (n >> 1) & 1;
+        const bool ragged = c.ragged_end && c.i == (c.rev ? 0 : c.count - 1);
+        // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
+        ok = wait(&b.full_y[s], ph) && (!ragged || wait(&b.z_full, n & 1)) && wait(&b.full_x[s], ph) &&
+             wait(&b.a_free[d], dph ^ 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t xk = x_k + s * (K::XB >> 4), yk = y_k + s * (K::YB >> 4);
+#pragma unroll 1
+        for (int kk = 0; kk < DRP / 16; ++kk)
+            mma_bf16(tm + K::T_A + d * CT, xk + k_step(kk), yk + k_step(kk), idA, kk > 0);
+        mma_commit(&b.a_full[d]);
+        ++c.i;
+        ++c.n;
+    };
+    Cursor cur{(int)blockIdx.x, 0, -1, false, false, 0}, ahead = cur;
+    cur.i = ahead.i = 0;
+    if (!STATES && settle(ahead)) issue_pairs(ahead);
+    while (ok && settle(cur)) {
+        const uint32_t n = cur.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, one = n & 1;
+        const uint64_t xk = x_k + s * (K::XB >> 4), ymn = y_mn + s * (K::YB >> 4), zmn = z_mn + s * (K::ZB >> 4);
+        ++cur.i;
+        ++cur.n;
+        if (!(ok = wait(&b.full_y[s], ph) && wait(&b.z_full, one) && wait(&b.d_free, one ^ 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int kk = 0; kk < CT / 16; ++kk)   // Zh and Zl are the two panels of one operand of 128 columns
+            mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk, idD, kk > 0);
+        mma_commit(&b.d_full);
+        mma_commit(&b.empty_y[s]);
+        if (STATES) {
+            mma_commit(&b.empty_z[s]);
+            continue;
+        }
+        if (settle(ahead)) issue_pairs(ahead);
+        if (!(ok = ok && wait(&b.s_full, one) && wait(&b.o_free, one ^ 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int kk = 0; kk < DRP / 16; ++kk)
+            mma_bf16(tm + K::T_O1, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
+        mma_commit(&b.s_free);
+        mma_commit(&b.empty_x[s]);
+        if (!(ok = wait(&b.full_z[s], ph) && wait(&b.p_full[d], (n >> 1) & 1))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int kk = 0; kk < CT / 16; ++kk)
+            mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
+        mma_commit(&b.o_full);
+        mma_commit(&b.a_free[d]);
+        mma_commit(&b.empty_z[s]);
     }
     if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
     // what was issued ends before TMEM is given back
     mma_commit(&b.drain);
-    mbar_wait(&b.drain, 0);
+    wait(&b.drain, 0);
 }
 
 // ------------------------------------------------------------ warpgroup 1: A -> P
 
-// Row i = 32 w + lane against column blocks of 32. Off the diagonal block a^|i-j| is a row part times a column part,
-// both with exponents >= 0 (border of the column block next to the diagonal); on it the power comes from a table.
+// Row i = 32 w + lane against column blocks of 32, those on the causal side.
+//
+// Mild decays (a >= 1/4, MILD): a^|i-j| = a^(row part) a^(column part), the row part (lane, or 31 - lane backwards) left
+// to the outputs, the column part 32 |w - jb| -+ j + const between -31 and 96: one value a column for all lanes, read
+// four at a time, and growing to 2^62 at most, which P (8-bit exponents) and the sum take. pw[pos] holds it by position.
+// Stronger decays would overflow it: their weights are read by distance, pw[128 + i - j], 0 off the causal side.
+constexpr float MILD = -2.f;   // log2 of the decay
 template <int DRP>
-__device__ void weigh_pairs(const Params& p, uint32_t tm, Bars& b, float* tab) {
+__device__ void weigh_pairs(const Params& p, uint32_t tm, Bars& b, float* pw) {
     using K = Cfg<DRP, false>;
-    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int w = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     uint32_t n = 0;
-    for (long long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    bool ok = true;
+    for (int x = blockIdx.x; x < p.items; x += gridDim.x) {
         const Item t = item_of<false>(p, x);
-        const bool rev = t.p->rev;
-        __syncwarp();
-        tab[lane] = linear::decay_pow(t.l2, lane);   // this warp's own table of a^0 .. a^31
-        __syncwarp();
-        for (int i = 0; i < t.count(); ++i, ++n) {
-            if (!warp_wait(&b.a_full[n & 1], (n >> 1) & 1)) return;
+        if (t.count() == 0) continue;
+        const bool rev = t.p->rev, mild = t.l2 >= MILD;
+        if (named_sync_or(2, 128, !ok)) return;      // the last item's weights have been read
+        if (mild) {
+            pw[rev ? 127 - tid : tid] = exp2f(t.l2 * (float)(96 - tid));
+        } else {
+            pw[128 + (rev ? -tid : tid)] = linear::decay_pow(t.l2, tid);
+            if (tid) pw[128 + (rev ? tid : -tid)] = 0.f;
+        }
+        named_sync(2, 128);
+        const int from = rev ? w : 0, to = rev ? 3 : w;
+        for (int i = 0; ok && i < t.count(); ++i, ++n) {
+            if (!(ok = warp_wait(&b.a_full[n & 1], (n >> 1) & 1))) break;
             tc_fence_after();
             const uint32_t ta = tm + K::T_A + (n & 1) * CT + ((uint32_t)(32 * w) << 16);
-#pragma unroll
+            // columns 16 jb .. of P lie in A's columns below 32 jb + 32, which this warp has read or does not need
+#pragma unroll 1
             for (int jb = 0; jb < 4; ++jb) {
-                float v[32], o[16];
-                if (rev ? jb < w : jb > w) {
+                float o[16];
+                if (jb < from || jb > to) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = 0.f;
                 } else {
-                    tmem_ld32(ta + 32 * jb, v);
-                    tmem_wait_ld(v);
-                    if (jb == w) {
+                    float u[32];
+                    tmem_ld32(ta + 32 * jb, u);
+                    if (mild) {
+                        const float4* q = reinterpret_cast<const float4*>(pw + 32 * (rev ? jb - w : 3 - w + jb));
+                        tmem_wait_ld(u);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int far = rev ? j - lane : lane - j;
-                            v[j] = far >= 0 ? v[j] * tab[far & 31] : 0.f;
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 c = q[j];
+                            const float2 lo = mul2(make_float2(u[4 * j], u[4 * j + 1]), make_float2(c.x, c.y));
+                            const float2 hi = mul2(make_float2(u[4 * j + 2], u[4 * j + 3]), make_float2(c.z, c.w));
+                            o[2 * j] = __uint_as_float(pack_bf16x2(lo.x, lo.y));
+                            o[2 * j + 1] = __uint_as_float(pack_bf16x2(hi.x, hi.y));
+                        }
+                        if (jb == w) {   // the bits of the pairs on the causal side: j <= lane, backwards j >= lane
+                            const uint32_t keep = rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const uint32_t m = ((keep >> (2 * j)) & 1u ? 0xffffu : 0u) | ((keep >> (2 * j + 1)) & 1u ? 0xffff0000u : 0u);
+                                o[j] = __uint_as_float(__float_as_uint(o[j]) & m);
+                            }
                         }
                     } else {
-                        const float row = linear::decay_pow(t.l2, rev ? 32 * (jb - w) - lane : 32 * (w - jb) + lane - 31);
+                        const float* q = pw + 128 + tid - 32 * jb;
+                        tmem_wait_ld(u);
 #pragma unroll
-                        for (int j4 = 0; j4 < 8; ++j4) {
-                            // column parts: a^(31-j) forwards, a^j backwards
-                            const float4 c = *reinterpret_cast<const float4*>(tab + (rev ? 4 * j4 : 28 - 4 * j4));
-                            v[4 * j4 + 0] *= row * (rev ? c.x : c.w);
-                            v[4 * j4 + 1] *= row * (rev ? c.y : c.z);
-                            v[4 * j4 + 2] *= row * (rev ? c.z : c.y);
-                            v[4 * j4 + 3] *= row * (rev ? c.w : c.x);
-                        }
+                        for (int j = 0; j < 16; ++j)
+                            o[j] = __uint_as_float(pack_bf16x2(u[2 * j] * q[-2 * j], u[2 * j + 1] * q[-2 * j - 1]));
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(pack_bf16x2(v[2 * j], v[2 * j + 1]));
                 }
-                // columns 16 jb .. of P lie in A's columns up to 32 jb + 31, which this warp has read
                 tmem_st16(ta + 16 * jb, o);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&b.p_full);
+            mbar_arrive(&b.p_full[n & 1]);
         }
     }
 }
 
 // ------------------------------------------------------------ warpgroup 2: g_j z_j in two terms
 
+// z (gh + gl) as hi + lo, two values at a time in bf16 arithmetic: hi is the rounded product, and its remainder
+// z gh - hi fits bf16 but for its last bit (8 x 8-bit products). The weight, its remainder and lo's rounding leave
+// 2^-18 each, as the split of a 32-bit product would, in half the instructions.
+__device__ __forceinline__ void two_terms(uint32_t z2, __nv_bfloat162 gh, __nv_bfloat162 gl, uint32_t* hi2, uint32_t* lo2) {
+    const __nv_bfloat162 z = *reinterpret_cast<__nv_bfloat162*>(&z2);
+    const __nv_bfloat162 hi = __hfma2(z, gh, __hmul2(z, gl));
+    const __nv_bfloat162 lo = __hfma2(z, gl, __hfma2(z, gh, __hneg2(hi)));
+    *hi2 = *reinterpret_cast<const uint32_t*>(&hi);
+    *lo2 = *reinterpret_cast<const uint32_t*>(&lo);
+}
+
 template <int DRP, bool STATES>
 __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
     const int j = threadIdx.x & 127;
     uint32_t n = 0;
-    for (long long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    for (int x = blockIdx.x; x < p.items; x += gridDim.x) {
         const Item t = item_of<STATES>(p, x);
         for (int i = 0; i < t.count(); ++i, ++n) {
             const uint32_t s = n % K::STAGES, ph = (n / K::STAGES) & 1;
@@ -305,30 +434,37 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
             if (!warp_wait(&b.full_z[s], ph)) return;
             if (valid < CT && !warp_wait(&b.full_y[s], ph)) return;
             // Zh and Zl are free once the last chunk's D is done
-            if (n > 0 && !warp_wait(&b.d_full[(n - 1) & 1], ((n - 1) >> 1) & 1)) return;
+            if (n > 0 && !warp_wait(&b.d_full, (n - 1) & 1)) return;
             if (j < valid) {
                 const float g = linear::decay_pow(t.l2, t.p->rev ? j + 1 : valid - 1 - j);
+                const __nv_bfloat162 gh = __float2bfloat162_rn(g), gl = __float2bfloat162_rn(g - __low2float(gh));
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint4 row[4];   // loads first: the stores below could not be told apart from later ones
 #pragma unroll
-                for (int c = 0; c < SL / 8; ++c) {
-                    float v[8], r[8];
-                    ld_row8(Z, CT, j, c, v);
+                    for (int c = 0; c < 4; ++c) row[c] = *reinterpret_cast<const uint4*>(Z + tile_chunk_off(CT, j, 4 * half + c));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] *= g;
-                        r[e] = v[e] - __bfloat162float(__float2bfloat16_rn(v[e]));
+                    for (int c = 0; c < 4; ++c) {
+                        uint4 hi, lo;
+                        two_terms(row[c].x, gh, gl, &hi.x, &lo.x);
+                        two_terms(row[c].y, gh, gl, &hi.y, &lo.y);
+                        two_terms(row[c].z, gh, gl, &hi.z, &lo.z);
+                        two_terms(row[c].w, gh, gl, &hi.w, &lo.w);
+                        const uint32_t at = tile_chunk_off(CT, j, 4 * half + c);
+                        *reinterpret_cast<uint4*>(Zh + at) = hi;
+                        *reinterpret_cast<uint4*>(Zl + at) = lo;
                     }
-                    st_row8(Zh, CT, j, c, v);
-                    st_row8(Zl, CT, j, c, r);
                 }
             } else {
                 const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < SL / 8; ++c) {
                     const uint32_t at = tile_chunk_off(CT, j, c);
                     *reinterpret_cast<uint4*>(Zh + at) = zero;
                     *reinterpret_cast<uint4*>(Zl + at) = zero;
                     *reinterpret_cast<uint4*>(Z + at) = zero;
                 }
+#pragma unroll 1
                 for (int c = 0; c < DRP / 8; ++c)
                     *reinterpret_cast<uint4*>(sm + K::OFF_Y + s * K::YB + tile_chunk_off(CT, j, c)) = zero;
             }
@@ -349,30 +485,32 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
     const Pass& q = *t.p;
     const size_t head = (size_t)t.n * p.seq.H + t.h;
     const int seg_tokens = p.cps * CT, nseg = (t.nc + p.cps - 1) / p.cps;
-    if (q.start && r < p.dr) {
-        // tokens between the sequence's end that the state stands at and this segment
-        const long long away = q.rev ? max(0ll, t.len - (t.seg + 1ll) * seg_tokens) : (long long)t.seg * seg_tokens;
+    // the start state under its decay, then the segments' states between it and here, each under its own
+    const int from = q.rev ? t.seg + 1 : 0, to = q.rev ? nseg : t.seg;
+#pragma unroll 1
+    for (int o = from - 1; o < max(from, to); ++o) {
+        const bool first = o < from;
+        if (first && (!q.start || r >= p.dr)) continue;
+        // tokens between where that state stands and this segment
+        const long long away = !first ? (long long)(q.rev ? o - t.seg - 1 : t.seg - 1 - o) * seg_tokens
+                               : q.rev ? max(0ll, t.len - (t.seg + 1ll) * seg_tokens) : (long long)t.seg * seg_tokens;
         const float f = linear::decay_pow(t.l2, (int)away);
-        const float* src = q.start + head * p.dr * p.dz;
-        if (q.start_transposed) {
-#pragma unroll
-            for (int j = 0; j < SL; ++j)
-                if (t.slice * SL + j < p.dz) S[j] = f * src[(size_t)(t.slice * SL + j) * p.dr + r];
-        } else {
+        if (first && !q.start_transposed) {
+            const float* src = q.start + (head * p.dr + r) * p.dz + t.slice * SL;
 #pragma unroll
             for (int j = 0; j < SL; j += 4)
                 if (t.slice * SL + j < p.dz) {
-                    const float4 v = *reinterpret_cast<const float4*>(src + (size_t)r * p.dz + t.slice * SL + j);
+                    const float4 v = *reinterpret_cast<const float4*>(src + j);
                     S[j] = f * v.x; S[j + 1] = f * v.y; S[j + 2] = f * v.z; S[j + 3] = f * v.w;
                 }
-        }
-    }
-    const int from = q.rev ? t.seg + 1 : 0, to = q.rev ? nseg : t.seg;
-    for (int o = from; o < to; ++o) {
-        const float f = linear::decay_pow(t.l2, (q.rev ? o - t.seg - 1 : t.seg - 1 - o) * seg_tokens);
-        const float* src = q.seg + ((head * p.nseg + o) * p.slices + t.slice) * (size_t)(SL * DRP) + r;
+        } else {   // columns contiguous over the rows
+            const float* src = first ? q.start + (head * p.dz + t.slice * SL) * p.dr + r
+                                     : q.seg + ((head * p.nseg + o) * p.slices + t.slice) * (size_t)(SL * DRP) + r;
+            const int step = first ? p.dr : DRP, cols = first ? p.dz - t.slice * SL : SL;
 #pragma unroll
-        for (int j = 0; j < SL; ++j) S[j] = fmaf(f, src[j * DRP], S[j]);
+            for (int j = 0; j < SL; ++j)
+                if (j < cols) S[j] = fmaf(f, src[j * step], S[j]);
+        }
     }
 }
 
@@ -395,7 +533,7 @@ __device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm,
         mbar_arrive(&b.s_full);
     };
     bool ok = true;
-    for (long long x = blockIdx.x; ok && x < p.items; x += gridDim.x) {
+    for (int x = blockIdx.x; ok && x < p.items; x += gridDim.x) {
         const Item t = item_of<STATES>(p, x);
         const bool last_seg = t.p->rev ? t.seg == 0 : t.seg == max(0, (t.nc + p.cps - 1) / p.cps - 1);
         const bool writes_end = !STATES && t.p->end && last_seg;
@@ -407,21 +545,26 @@ __device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm,
         }
         for (int i = 0; i < t.count(); ++i, ++n) {
             const int c = t.chunk(i), valid = t.valid(c);
-            const uint32_t d = n & 1, dph = (n >> 1) & 1;
-            ok = ok && warp_wait(&b.d_full[d], dph);
+            ok = ok && warp_wait(&b.d_full, n & 1);
             if (ok) {
                 tc_fence_after();
                 const float aC = linear::decay_pow(t.l2, valid);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float D[32];
-                    tmem_ld32(tm + K::T_D + d * SL + 32 * h + quarter, D);
-                    tmem_wait_ld(D);
+                for (int h = 0; h < 4; ++h) {
+                    float hi[16], lo[16];
+                    tmem_ld16(tm + K::T_D + 16 * h + quarter, hi);
+                    tmem_ld16(tm + K::T_D + SL + 16 * h + quarter, lo);
+                    tmem_wait_ld(hi, lo);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) S[32 * h + j] = fmaf(aC, S[32 * h + j], D[j]);
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 v = fma2(make_float2(aC, aC), make_float2(S[16 * h + j], S[16 * h + j + 1]),
+                                              add2(make_float2(hi[j], hi[j + 1]), make_float2(lo[j], lo[j + 1])));
+                        S[16 * h + j] = v.x;
+                        S[16 * h + j + 1] = v.y;
+                    }
                 }
                 tc_fence_before();
-                mbar_arrive(&b.d_free[d]);
+                mbar_arrive(&b.d_free);
                 if (!STATES && i + 1 < t.count()) {
                     ok = warp_wait(&b.s_free, n & 1);
                     if (ok) copy_state();
@@ -440,14 +583,21 @@ __device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm,
             {
                 const int orow = 32 * w + lane;
                 const float f = linear::decay_pow(t.l2, t.p->rev ? max(0, valid - 1 - orow) : orow + 1);
-#pragma unroll
+                // the row part of the pair weights (weigh_pairs)
+                const float e = t.l2 >= MILD ? linear::decay_pow(t.l2, t.p->rev ? 31 - lane : lane) : 1.f;
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     float o1[16], o2[16];
                     tmem_ld16(tm + K::T_O1 + 16 * h + quarter, o1);
                     tmem_ld16(tm + K::T_O2 + 16 * h + quarter, o2);
                     tmem_wait_ld(o1, o2);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o2[j] = fmaf(f, o1[j], o2[j]);
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 v = fma2(make_float2(f, f), make_float2(o1[j], o1[j + 1]),
+                                              mul2(make_float2(e, e), make_float2(o2[j], o2[j + 1])));
+                        o2[j] = v.x;
+                        o2[j + 1] = v.y;
+                    }
                     st_row8(Ob, CT, orow, 2 * h, o2);
                     st_row8(Ob, CT, orow, 2 * h + 1, o2 + 8);
                 }
@@ -494,7 +644,7 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     unsigned char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     __shared__ Bars b;
     __shared__ uint32_t tmem;
-    __shared__ __align__(16) float tab[4][32];
+    __shared__ __align__(16) float pw[256];
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 3; ++s) {
@@ -502,10 +652,10 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
             mbar_init(&b.empty_x[s], 1); mbar_init(&b.empty_y[s], 1); mbar_init(&b.empty_z[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.d_full[i], 1); mbar_init(&b.d_free[i], 128);
-            mbar_init(&b.a_full[i], 1); mbar_init(&b.a_free[i], 1);
+            mbar_init(&b.a_full[i], 1); mbar_init(&b.a_free[i], 1); mbar_init(&b.p_full[i], 128);
         }
-        mbar_init(&b.p_full, 128); mbar_init(&b.z_full, 128);
+        mbar_init(&b.z_full, 128);
+        mbar_init(&b.d_full, 1); mbar_init(&b.d_free, 128);
         mbar_init(&b.s_full, 128); mbar_init(&b.s_free, 1);
         mbar_init(&b.o_full, 1); mbar_init(&b.o_free, 128);
         mbar_init(&b.drain, 1);
@@ -520,13 +670,13 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tm = tmem;
     if (warp == 0) {
-        if (threadIdx.x == 0) load_tiles<DRP, STATES>(p, sm, b);
+        if (elect_one()) load_tiles<DRP, STATES>(p, sm, b);
         __syncwarp();
     } else if (warp == 1) {
-        if (threadIdx.x == 32) issue_products<DRP, STATES>(p, sm, tm, b);
+        if (elect_one()) issue_products<DRP, STATES>(p, sm, tm, b);
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
-        if constexpr (!STATES) weigh_pairs<DRP>(p, tm, b, tab[warp & 3]);
+        if constexpr (!STATES) weigh_pairs<DRP>(p, tm, b, pw);
     } else if (warp >= 8 && warp < 12) split_values<DRP, STATES>(p, sm, b);
     else if (warp >= 12) carry_and_write<DRP, STATES>(p, sm, tm, b);
     tc_fence_before();
@@ -603,9 +753,9 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     using K = Cfg<DRP, STATES>;
     cudaError_t e = cudaFuncSetAttribute(linear_chunk_kernel<DRP, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
     if (e != cudaSuccess) return e;
-    const long long grid = std::min<long long>(p.items, sm_count());
+    const int grid = std::min(p.items, sm_count());
     TraceScope trace(STATES ? K_LINEAR_SEGMENT : K_LINEAR_CHUNK, s);
-    linear_chunk_kernel<DRP, STATES><<<(unsigned)grid, NT, K::SMEM, s>>>(p);
+    linear_chunk_kernel<DRP, STATES><<<grid, NT, K::SMEM, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -620,7 +770,9 @@ cudaError_t run_group(const LinearArgs& a, const Group& g, const Cut& cut, cudaS
     p.slices = slices_of(g.dz);
     p.nseg = cut.nseg;
     p.cps = cut.cps;
-    p.items = (long long)cut.nseg * a.seq.N * a.seq.H * g.npass * p.slices;
+    const long long items = (long long)cut.nseg * a.seq.N * a.seq.H * g.npass * p.slices;
+    if (items > 2000000000ll) return cudaErrorInvalidConfiguration;
+    p.items = (int)items;
     cudaError_t e = cudaSuccess;
     if (cut.nseg > 1) e = padded(g.dr) == 128 ? launch<128, true>(p, s) : launch<64, true>(p, s);
     if (e != cudaSuccess) return e;
