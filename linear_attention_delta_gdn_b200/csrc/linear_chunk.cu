@@ -13,8 +13,8 @@
 // a 32-bit result, so g_j z_j goes into D as two bf16 terms, hi and the rest: 2^-18, where one term would leave 2^-9
 // in a state that every later token reads. Sums are 32-bit.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P; warpgroup 2 makes Zh and Zl; warpgroup 3 keeps
-// the state and writes the outputs. A block takes work items (sequence, head, column slice, segment, pass) in turn and
+// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P; warpgroup 2 makes Zh and Zl and writes
+// the outputs; warpgroup 3 keeps the state. A block takes work items (sequence, head, column slice, segment, pass) in turn and
 // the warps run ahead of one another across items.
 //
 // Few heads: a sequence's chunks are cut into segments of whole chunks, each an item of its own. A first launch leaves
@@ -46,7 +46,8 @@ constexpr int NT = 512;         // threads of a block
 constexpr int MAX_PASS = 3;
 
 struct Pass {
-    CUtensorMap x, y, z, out;
+    CUtensorMap x, y, out;
+    const void* z_ptr;
     const float* start;      // state in front of the first (behind the last) token, [N, H, Dk, Dv], or null
     float* end;              // the state at the other end, or null
     float* seg;              // the segments' own states, [N, H, seg, slice][SL][DRP], or null
@@ -109,19 +110,20 @@ struct Cfg {
     static constexpr uint32_t XB = STATES ? 0 : CT * DRP * 2;      // bytes of a row-operand tile
     static constexpr uint32_t YB = CT * DRP * 2;
     static constexpr uint32_t ZB = CT * SL * 2;
-    static constexpr int STAGES = (DRP == 128 && !STATES) ? 2 : 3;
+    static constexpr int STAGES = (DRP == 128 && !STATES) ? 2 : 4; // of X and Y
+    static constexpr int ZRAW = STATES ? 0 : 2;                    // Z as it is, for P Z
     static constexpr uint32_t SB = STATES ? 0 : DRP * SL * 2;      // bf16 copy of the state
     static constexpr uint32_t OB = STATES ? 0 : CT * SL * 2;       // output staging
-    static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + STAGES * ZB,
+    static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + ZRAW * ZB,
                               OFF_ZL = OFF_ZH + ZB, OFF_S = OFF_ZL + ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
     static constexpr uint32_t SMEM = TOTAL + 1024;                 // tiles start on 1024 bytes
-    // TMEM columns: A (then P in its first half) twice, D (its Zh and its Zl part), O1, O2
-    static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 384, T_O2 = 448;
+    // TMEM columns: A twice (then P in its first half and O1 in its second), D (its Zh and its Zl part), O2 twice
+    static constexpr uint32_t T_A = 0, T_O1 = 64, T_D = 256, T_O2 = 384;
 };
 
 struct Bars {
-    uint64_t full_x[3], full_y[3], full_z[3], empty_x[3], empty_y[3], empty_z[3];
-    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full, o_free, drain;
+    uint64_t full_x[4], full_y[4], empty_x[4], empty_y[4];
+    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full[2], o_free[2], drain;
 };
 
 // The chunk loops of five kinds of warps share one instruction cache, and a loop that runs through it straight costs
@@ -194,7 +196,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 template <int DRP, bool STATES>
 __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
-    uint32_t ny = 0, nx = 0, nz = 0;   // tiles asked for so far, over all items
+    uint32_t ny = 0, nx = 0;   // tiles asked for so far, over all items
     bool ok = true;
     for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
         const Item t = item_of<STATES>(p, it);
@@ -215,10 +217,6 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
                     tma_load_3d(sm + s * K::XB + c * CT * 128, &t.p->x, 64 * c, t.h, row, &b.full_x[s]);
                 ++nx;
             }
-            if (!(ok = wait(&b.empty_z[s], ph))) break;
-            mbar_arrive_expect_tx(&b.full_z[s], K::ZB);
-            tma_load_3d(sm + K::OFF_Z + s * K::ZB, &t.p->z, t.slice * SL, t.h, row, &b.full_z[s]);
-            ++nz;
         }
     }
     if (ok) return;   // every tile was waited for by those who read it
@@ -230,7 +228,6 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     };
     land(b.full_y, ny);
     land(b.full_x, nx);
-    land(b.full_z, nz);
 }
 
 // ------------------------------------------------------------ warp 1: products
@@ -250,7 +247,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     // K-major: 32 bytes a step within a panel of 64 columns, then the next panel
     auto k_step = [](int kk) { return (uint64_t)(((kk >> 2) * CT * 128 + (kk & 3) * 32) >> 4); };
     // Two cursors over the same chunks. A of the next chunk is issued before O1 and O2 of this one, so that turning it
-    // into P has the time of all the products in between.
+    // into P has the time of four products.
     struct Cursor {
         int x, i, count;
         bool ragged_end;   // the item's chunk range ends in a partial chunk
@@ -275,7 +272,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         const bool ragged = c.ragged_end && c.i == (c.rev ? 0 : c.count - 1);
         // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
         ok = wait(&b.full_y[s], ph) && (!ragged || wait(&b.z_full, n & 1)) && wait(&b.full_x[s], ph) &&
-             wait(&b.a_free[d], dph ^ 1);
+             wait(&b.a_free[d], dph ^ 1) && wait(&b.o_free[d], dph ^ 1);
         if (!ok) return;
         tc_fence_after();
         const uint64_t xk = x_k + s * (K::XB >> 4), yk = y_k + s * (K::YB >> 4);
@@ -291,7 +288,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     if (!STATES && settle(ahead)) issue_pairs(ahead);
     while (ok && settle(cur)) {
         const uint32_t n = cur.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, one = n & 1;
-        const uint64_t xk = x_k + s * (K::XB >> 4), ymn = y_mn + s * (K::YB >> 4), zmn = z_mn + s * (K::ZB >> 4);
+        const uint64_t xk = x_k + s * (K::XB >> 4), ymn = y_mn + s * (K::YB >> 4), zmn = z_mn + d * (K::ZB >> 4);
         ++cur.i;
         ++cur.n;
         if (!(ok = wait(&b.full_y[s], ph) && wait(&b.z_full, one) && wait(&b.d_free, one ^ 1))) break;
@@ -301,26 +298,21 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
             mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk, idD, kk > 0);
         mma_commit(&b.d_full);
         mma_commit(&b.empty_y[s]);
-        if (STATES) {
-            mma_commit(&b.empty_z[s]);
-            continue;
-        }
+        if (STATES) continue;
         if (settle(ahead)) issue_pairs(ahead);
-        if (!(ok = ok && wait(&b.s_full, one) && wait(&b.o_free, one ^ 1))) break;
+        // O1 takes the half of A that P leaves
+        if (!(ok = ok && wait(&b.s_full, one) && wait(&b.p_full[d], (n >> 1) & 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < DRP / 16; ++kk)
-            mma_bf16(tm + K::T_O1, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
+            mma_bf16(tm + K::T_O1 + d * CT, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
         mma_commit(&b.s_free);
         mma_commit(&b.empty_x[s]);
-        if (!(ok = wait(&b.full_z[s], ph) && wait(&b.p_full[d], (n >> 1) & 1))) break;
-        tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)
-            mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
-        mma_commit(&b.o_full);
+            mma_bf16_ts(tm + K::T_O2 + d * SL, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
+        mma_commit(&b.o_full[d]);
         mma_commit(&b.a_free[d]);
-        mma_commit(&b.empty_z[s]);
     }
     if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
     // what was issued ends before TMEM is given back
@@ -406,7 +398,7 @@ __device__ void weigh_pairs(const Params& p, uint32_t tm, Bars& b, float* pw) {
     }
 }
 
-// ------------------------------------------------------------ warpgroup 2: g_j z_j in two terms
+// ------------------------------------------------------------ warpgroup 2: g_j z_j in two terms, the outputs
 
 // z (gh + gl) as hi + lo, two values at a time in bf16 arithmetic: hi is the rounded product, and its remainder
 // z gh - hi fits bf16 but for its last bit (8 x 8-bit products). The weight, its remainder and lo's rounding leave
@@ -419,62 +411,160 @@ __device__ __forceinline__ void two_terms(uint32_t z2, __nv_bfloat162 gh, __nv_b
     *lo2 = *reinterpret_cast<const uint32_t*>(&lo);
 }
 
-template <int DRP, bool STATES>
-__device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
-    using K = Cfg<DRP, STATES>;
-    const int j = threadIdx.x & 127;
-    uint32_t n = 0;
-    for (int x = blockIdx.x; x < p.items; x += gridDim.x) {
-        const Item t = item_of<STATES>(p, x);
-        for (int i = 0; i < t.count(); ++i, ++n) {
-            const uint32_t s = n % K::STAGES, ph = (n / K::STAGES) & 1;
-            const int valid = t.valid(t.chunk(i));
-            unsigned char* Z = sm + K::OFF_Z + s * K::ZB;
-            unsigned char *Zh = sm + K::OFF_ZH, *Zl = sm + K::OFF_ZL;
-            if (!warp_wait(&b.full_z[s], ph)) return;
-            if (valid < CT && !warp_wait(&b.full_y[s], ph)) return;
-            // Zh and Zl are free once the last chunk's D is done
-            if (n > 0 && !warp_wait(&b.d_full, (n - 1) & 1)) return;
-            if (j < valid) {
-                const float g = linear::decay_pow(t.l2, t.p->rev ? j + 1 : valid - 1 - j);
-                const __nv_bfloat162 gh = __float2bfloat162_rn(g), gl = __float2bfloat162_rn(g - __low2float(gh));
+// A chunk's outputs, 32 rows a warp: o = f O1 + e O2 with f the power between the state's border and the row, e the row
+// part of the pair weights (weigh_pairs).
+struct Out {
+    const Pass* p;
+    int row, valid, h, slice;
+    float l2;
+};
+template <int DRP>
+__device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uint32_t n, unsigned char* sm, uint32_t tm, Bars& b) {
+    using K = Cfg<DRP, false>;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, orow = 32 * w + lane;
+    const bool rev = q.p->rev;
+    unsigned char* Ob = sm + K::OFF_O + w * (K::OB / 4);   // this warp's 32 rows
+    const uint32_t d = n & 1;
+    if (!warp_wait(&b.o_full[d], (n >> 1) & 1)) return false;
+    tc_fence_after();
+    if (lane == 0) bulk_wait_read();   // the last store has read them
+    __syncwarp();
+    const float f = linear::decay_pow(q.l2, rev ? max(0, q.valid - 1 - orow) : orow + 1);
+    const float e = q.l2 >= MILD ? linear::decay_pow(q.l2, rev ? 31 - lane : lane) : 1.f;
+    const uint32_t quarter = (uint32_t)(32 * w) << 16;
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint4 row[4];   // loads first: the stores below could not be told apart from later ones
+    for (int k = 0; k < 4; ++k) {
+        float o1[16], o2[16];
+        tmem_ld16(tm + K::T_O1 + d * CT + 16 * k + quarter, o1);
+        tmem_ld16(tm + K::T_O2 + d * SL + 16 * k + quarter, o2);
+        tmem_wait_ld(o1, o2);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) row[c] = *reinterpret_cast<const uint4*>(Z + tile_chunk_off(CT, j, 4 * half + c));
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint4 hi, lo;
-                        two_terms(row[c].x, gh, gl, &hi.x, &lo.x);
-                        two_terms(row[c].y, gh, gl, &hi.y, &lo.y);
-                        two_terms(row[c].z, gh, gl, &hi.z, &lo.z);
-                        two_terms(row[c].w, gh, gl, &hi.w, &lo.w);
-                        const uint32_t at = tile_chunk_off(CT, j, 4 * half + c);
-                        *reinterpret_cast<uint4*>(Zh + at) = hi;
-                        *reinterpret_cast<uint4*>(Zl + at) = lo;
-                    }
-                }
-            } else {
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-                for (int c = 0; c < SL / 8; ++c) {
-                    const uint32_t at = tile_chunk_off(CT, j, c);
-                    *reinterpret_cast<uint4*>(Zh + at) = zero;
-                    *reinterpret_cast<uint4*>(Zl + at) = zero;
-                    *reinterpret_cast<uint4*>(Z + at) = zero;
-                }
-#pragma unroll 1
-                for (int c = 0; c < DRP / 8; ++c)
-                    *reinterpret_cast<uint4*>(sm + K::OFF_Y + s * K::YB + tile_chunk_off(CT, j, c)) = zero;
-            }
-            fence_async_smem();
-            mbar_arrive(&b.z_full);
+        for (int j = 0; j < 16; j += 2) {
+            const float2 v = fma2(make_float2(f, f), make_float2(o1[j], o1[j + 1]), mul2(make_float2(e, e), make_float2(o2[j], o2[j + 1])));
+            o2[j] = v.x;
+            o2[j + 1] = v.y;
         }
+        st_row8(Ob, 32, lane, 2 * k, o2);
+        st_row8(Ob, 32, lane, 2 * k + 1, o2 + 8);
     }
+    tc_fence_before();
+    mbar_arrive(&b.o_free[d]);
+    if (q.valid == CT) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&q.p->out, q.slice * SL, q.h, q.row + 32 * w, Ob);
+            bulk_commit();
+        }
+    } else {   // the rows behind the end are not this sequence's: 16-byte pieces of the real ones
+        __syncwarp();
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(q.p->out_ptr);
+#pragma unroll 1
+        for (int x = lane; x < 32 * (SL / 8); x += 32) {
+            const int rr = x / (SL / 8), cc = x % (SL / 8);
+            if (32 * w + rr < q.valid && q.slice * SL + 8 * cc < p.dz)
+                *reinterpret_cast<uint4*>(out + ((size_t)(q.row + 32 * w + rr) * p.seq.H + q.h) * p.dz + q.slice * SL + 8 * cc) =
+                    *reinterpret_cast<const uint4*>(Ob + tile_chunk_off(32, rr, cc));
+        }
+        __syncwarp();
+    }
+    return true;
 }
 
-// ------------------------------------------------------------ warpgroup 3: the state, the outputs
+// Z does not come through TMA: its rows go from global memory to registers a chunk ahead (eight lanes a row), and from
+// there to shared memory as they are and as the two terms. Nothing then waits for a stage to be given back.
+template <int DRP, bool STATES>
+__device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t tm, Bars& b) {
+    using K = Cfg<DRP, STATES>;
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+    const int r0 = 32 * w + (lane >> 3), c = lane & 7;   // rows r0 + 4 k, 16-byte piece c
+    uint32_t n = 0;
+    Item t;
+    int x = blockIdx.x, i = -1;
+    auto next = [&]() {   // to the next chunk, over items; false behind the last
+        ++i;
+        if (n == 0 && i == 0 && x < p.items) t = item_of<STATES>(p, x);
+        while (x < p.items && i >= t.count()) {
+            x += gridDim.x;
+            i = 0;
+            if (x < p.items) t = item_of<STATES>(p, x);
+        }
+        return x < p.items;
+    };
+    uint4 ahead[8];
+    auto load = [&]() {
+        const int valid = t.valid(t.chunk(i)), col = t.slice * SL + 8 * c;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(t.p->z_ptr) + ((t.row0 + (long long)t.chunk(i) * CT + r0) * p.seq.H + t.h) * p.dz + col);
+        const size_t step = (size_t)4 * p.seq.H * p.dz / 8;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ahead[k] = r0 + 4 * k < valid && col < p.dz ? __ldg(src + k * step) : make_uint4(0, 0, 0, 0);
+    };
+    bool more = next();
+    if (more) load();
+    __nv_bfloat162 gh[8], gl[8];   // the rows' weights
+    int have = -1, have_x = -1;
+    Out out{};   // of the chunk before: its outputs are written once this one's values are on their way
+    bool ok = true;
+    while (more) {
+        const int valid = t.valid(t.chunk(i));
+        const float l2 = t.l2;
+        const bool rev = t.p->rev;
+        if (valid != have || x != have_x) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + 4 * k;
+                const float g = linear::decay_pow(l2, rev ? r + 1 : max(0, valid - 1 - r));
+                gh[k] = __float2bfloat162_rn(g);
+                gl[k] = __float2bfloat162_rn(g - __low2float(gh[k]));
+            }
+            have = valid;
+            have_x = x;
+        }
+        uint4 z[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] = ahead[k];
+        const Out mine{t.p, (int)(t.row0 + (long long)t.chunk(i) * CT), valid, t.h, t.slice, l2};
+        more = next();
+        if (more) load();
+        // Zh and Zl are free once the last chunk's D is done, this copy of Z once the chunk before that has its O2
+        if (!(ok = n == 0 || warp_wait(&b.d_full, (n - 1) & 1))) break;
+        if (!STATES && !(ok = warp_wait(&b.a_free[n & 1], ((n >> 1) & 1) ^ 1))) break;
+        unsigned char* Z = sm + K::OFF_Z + (n & 1) * K::ZB;
+        unsigned char *Zh = sm + K::OFF_ZH, *Zl = sm + K::OFF_ZL;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint4 hi, lo;
+            two_terms(z[k].x, gh[k], gl[k], &hi.x, &lo.x);
+            two_terms(z[k].y, gh[k], gl[k], &hi.y, &lo.y);
+            two_terms(z[k].z, gh[k], gl[k], &hi.z, &lo.z);
+            two_terms(z[k].w, gh[k], gl[k], &hi.w, &lo.w);
+            const uint32_t at = tile_chunk_off(CT, r0 + 4 * k, c);
+            *reinterpret_cast<uint4*>(Zh + at) = hi;
+            *reinterpret_cast<uint4*>(Zl + at) = lo;
+            if (!STATES) *reinterpret_cast<uint4*>(Z + at) = z[k];
+        }
+        if (valid < CT) {   // rows of Y behind the sequence's end: they are another's, and would meet the zeros of Z
+            const uint32_t s = n % K::STAGES;
+            if (!(ok = warp_wait(&b.full_y[s], (n / K::STAGES) & 1))) break;
+            if (tid >= valid)
+#pragma unroll 1
+                for (int q = 0; q < DRP / 8; ++q)
+                    *reinterpret_cast<uint4*>(sm + K::OFF_Y + s * K::YB + tile_chunk_off(CT, tid, q)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        mbar_arrive(&b.z_full);
+        if (!STATES && n > 0 && !(ok = write_outputs<DRP>(p, out, n - 1, sm, tm, b))) break;
+        out = mine;
+        ++n;
+    }
+    if (STATES) return;
+    if (ok && n > 0) write_outputs<DRP>(p, out, n - 1, sm, tm, b);
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+}
+
+// ------------------------------------------------------------ warpgroup 3: the state
 
 // Start state of an item: row r of the slice's columns.
 template <int DRP, bool STATES>
@@ -515,14 +605,14 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
 }
 
 template <int DRP, bool STATES>
-__device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm, Bars& b) {
+__device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bars& b) {
     using K = Cfg<DRP, STATES>;
-    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
+    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     // accumulator rows: 128 in lanes 0..127; 64 in the first 16 lanes of each quarter
     const int r = DRP == 128 ? 32 * w + lane : 16 * w + (lane & 15);
     const bool real = DRP == 128 || lane < 16;
     const uint32_t quarter = (uint32_t)(32 * w) << 16;
-    unsigned char *Sb = sm + K::OFF_S, *Ob = sm + K::OFF_O;
+    unsigned char* Sb = sm + K::OFF_S;
     uint32_t n = 0;
     float S[SL];
     auto copy_state = [&]() {   // the bf16 copy that the next O1 reads
@@ -570,56 +660,7 @@ __device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm,
                     if (ok) copy_state();
                 }
             }
-            if (STATES) {
-                if (!ok) break;
-                continue;
-            }
-            ok = ok && warp_wait(&b.o_full, n & 1);
-            const int row = (int)(t.row0 + (long long)c * CT);
-            if (tid == 0) bulk_wait_read();   // the staging tile's last store has been read
-            ok = !named_sync_or(1, 128, !ok);
             if (!ok) break;
-            tc_fence_after();
-            {
-                const int orow = 32 * w + lane;
-                const float f = linear::decay_pow(t.l2, t.p->rev ? max(0, valid - 1 - orow) : orow + 1);
-                // the row part of the pair weights (weigh_pairs)
-                const float e = t.l2 >= MILD ? linear::decay_pow(t.l2, t.p->rev ? 31 - lane : lane) : 1.f;
-#pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
-                    float o1[16], o2[16];
-                    tmem_ld16(tm + K::T_O1 + 16 * h + quarter, o1);
-                    tmem_ld16(tm + K::T_O2 + 16 * h + quarter, o2);
-                    tmem_wait_ld(o1, o2);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 v = fma2(make_float2(f, f), make_float2(o1[j], o1[j + 1]),
-                                              mul2(make_float2(e, e), make_float2(o2[j], o2[j + 1])));
-                        o2[j] = v.x;
-                        o2[j + 1] = v.y;
-                    }
-                    st_row8(Ob, CT, orow, 2 * h, o2);
-                    st_row8(Ob, CT, orow, 2 * h + 1, o2 + 8);
-                }
-                tc_fence_before();
-                mbar_arrive(&b.o_free);
-            }
-            fence_async_smem();
-            named_sync(1, 128);
-            if (valid == CT) {
-                if (tid == 0) {
-                    tma_store_3d(&t.p->out, t.slice * SL, t.h, row, Ob);
-                    bulk_commit();
-                }
-            } else {   // the rows behind the end are not this sequence's: 16-byte pieces of the real rows
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(t.p->out_ptr);
-                for (int e = tid; e < valid * (SL / 8); e += 128) {
-                    const int rr = e / (SL / 8), cc = e % (SL / 8);
-                    if (t.slice * SL + 8 * cc < p.dz)
-                        *reinterpret_cast<uint4*>(out + ((size_t)(row + rr) * p.seq.H + t.h) * p.dz + t.slice * SL + 8 * cc) =
-                            *reinterpret_cast<const uint4*>(Ob + tile_chunk_off(CT, rr, cc));
-                }
-            }
         }
         if (!ok || !real) continue;
         if (STATES) {
@@ -633,8 +674,6 @@ __device__ void carry_and_write(const Params& p, unsigned char* sm, uint32_t tm,
                 if (t.slice * SL + j < p.dz) *reinterpret_cast<float4*>(dst + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
         }
     }
-    if (tid == 0) bulk_wait_all();
-    __syncwarp();
 }
 
 template <int DRP, bool STATES>
@@ -647,17 +686,17 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     __shared__ __align__(16) float pw[256];
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 3; ++s) {
-            mbar_init(&b.full_x[s], 1); mbar_init(&b.full_y[s], 1); mbar_init(&b.full_z[s], 1);
-            mbar_init(&b.empty_x[s], 1); mbar_init(&b.empty_y[s], 1); mbar_init(&b.empty_z[s], 1);
+        for (int s = 0; s < K::STAGES; ++s) {
+            mbar_init(&b.full_x[s], 1); mbar_init(&b.full_y[s], 1);
+            mbar_init(&b.empty_x[s], 1); mbar_init(&b.empty_y[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.a_full[i], 1); mbar_init(&b.a_free[i], 1); mbar_init(&b.p_full[i], 128);
+            mbar_init(&b.o_full[i], 1); mbar_init(&b.o_free[i], 128);
         }
         mbar_init(&b.z_full, 128);
         mbar_init(&b.d_full, 1); mbar_init(&b.d_free, 128);
         mbar_init(&b.s_full, 128); mbar_init(&b.s_free, 1);
-        mbar_init(&b.o_full, 1); mbar_init(&b.o_free, 128);
         mbar_init(&b.drain, 1);
         fence_mbar_init();
     }
@@ -677,15 +716,15 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         if constexpr (!STATES) weigh_pairs<DRP>(p, tm, b, pw);
-    } else if (warp >= 8 && warp < 12) split_values<DRP, STATES>(p, sm, b);
-    else if (warp >= 12) carry_and_write<DRP, STATES>(p, sm, tm, b);
+    } else if (warp >= 8 && warp < 12) values_and_outputs<DRP, STATES>(p, sm, tm, b);
+    else if (warp >= 12) carry_state<DRP, STATES>(p, sm, tm, b);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tm, 512);
 }
 
-CUresult encode(CUtensorMap* map, const void* ptr, const Seqs& s, int D) {
+CUresult encode(CUtensorMap* map, const void* ptr, const Seqs& s, int D, int rows) {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         cudaDriverEntryPointQueryResult q;
         void* f = nullptr;
@@ -693,10 +732,10 @@ CUresult encode(CUtensorMap* map, const void* ptr, const Seqs& s, int D) {
         return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
     }();
     if (!fn) return CUDA_ERROR_NOT_FOUND;
-    // [rows, H, D] in boxes of 128 rows x 1 head x 64 channels; channels behind D and rows behind the tensor read as 0
+    // [rows, H, D] in boxes of some rows x 1 head x 64 channels; channels behind D and rows behind the tensor read as 0
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)s.H, (cuuint64_t)s.Ttot};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)s.H * D * 2};
-    cuuint32_t box[3] = {64, 1, CT}, step[3] = {1, 1, 1};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -826,11 +865,12 @@ cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
     auto pass = [&](const void* x, int dr, const void* y, const void* z, int dz, void* out, const float* start, float* end,
                     bool transposed, bool rev) {
         Pass p{};
-        good = good && encode(&p.x, x, q, dr) == CUDA_SUCCESS && encode(&p.y, y, q, dr) == CUDA_SUCCESS &&
-               encode(&p.z, z, q, dz) == CUDA_SUCCESS && encode(&p.out, out, q, dz) == CUDA_SUCCESS;
+        good = good && encode(&p.x, x, q, dr, CT) == CUDA_SUCCESS && encode(&p.y, y, q, dr, CT) == CUDA_SUCCESS &&
+               encode(&p.out, out, q, dz, 32) == CUDA_SUCCESS;
         p.start = start;
         p.end = end;
         p.seg = seg(dr, dz);
+        p.z_ptr = z;
         p.out_ptr = out;
         p.start_transposed = transposed;
         p.rev = rev;
