@@ -5,7 +5,7 @@
 //     out = diag(f) X R + P Z,        R' = a^C R + Y^T diag(g) Z
 // A block owns 64 columns of Z (and of out and R), so a head of 128 is two blocks and 64 heads fill the GPU; X and Y
 // are then read by both, the second time from L2. Products per chunk and block (tcgen05, M = 128, 32-bit TMEM):
-//     A = X Y^T (N 128)    D = Y^T [Zh | Zl] (N 128)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
+//     A = X Y^T (N 128)    D = Y^T Zh + Y^T Zl (N 64)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
@@ -13,8 +13,8 @@
 // a 32-bit result, so g_j z_j goes into D as two bf16 terms, hi and the rest: 2^-18, where one term would leave 2^-9
 // in a state that every later token reads. Sums are 32-bit.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P; warpgroup 2 makes Zh and Zl and writes
-// the outputs; warpgroup 3 keeps the state. A block takes work items (sequence, head, column slice, segment, pass) in turn and
+// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P and writes the
+// outputs; warpgroup 2 makes Zh and Zl; warpgroup 3 keeps the state. A block takes work items (sequence, head, column slice, segment, pass) in turn and
 // the warps run ahead of one another across items.
 //
 // Few heads: a sequence's chunks are cut into segments of whole chunks, each an item of its own. A first launch leaves
@@ -117,13 +117,13 @@ struct Cfg {
     static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + ZRAW * ZB,
                               OFF_ZL = OFF_ZH + ZB, OFF_S = OFF_ZL + ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
     static constexpr uint32_t SMEM = TOTAL + 1024;                 // tiles start on 1024 bytes
-    // TMEM columns: A twice (then P in its first half and O1 in its second), D (its Zh and its Zl part), O2 twice
-    static constexpr uint32_t T_A = 0, T_O1 = 64, T_D = 256, T_O2 = 384;
+    // TMEM columns: A twice (then P in its first half), D, O1 twice, O2
+    static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 320, T_O2 = 448;
 };
 
 struct Bars {
     uint64_t full_x[4], full_y[4], empty_x[4], empty_y[4];
-    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full[2], o_free[2], drain;
+    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full, o_free, drain;
 };
 
 // The chunk loops of five kinds of warps share one instruction cache, and a loop that runs through it straight costs
@@ -241,7 +241,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     const uint64_t x_k = desc_k(base, CT, 0, 0), y_k = desc_k(base + K::OFF_Y, CT, 0, 0),
                    y_mn = desc_mn(base + K::OFF_Y, CT, 0, 0), z_mn = desc_mn(base + K::OFF_Z, CT, 0, 0),
                    zh_mn = desc_mn(base + K::OFF_ZH, CT, 0, 0), s_mn = desc_mn(base + K::OFF_S, DRP, 0, 0);
-    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, 2 * SL, true, true),
+    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, SL, true, true),
                    idO = idesc_bf16(128, SL, false, true);
     constexpr uint64_t MN = (16 * 128) >> 4;   // 16 rows of an MN-major tile
     // K-major: 32 bytes a step within a panel of 64 columns, then the next panel
@@ -272,7 +272,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         const bool ragged = c.ragged_end && c.i == (c.rev ? 0 : c.count - 1);
         // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
         ok = wait(&b.full_y[s], ph) && (!ragged || wait(&b.z_full, n & 1)) && wait(&b.full_x[s], ph) &&
-             wait(&b.a_free[d], dph ^ 1) && wait(&b.o_free[d], dph ^ 1);
+             wait(&b.a_free[d], dph ^ 1);
         if (!ok) return;
         tc_fence_after();
         const uint64_t xk = x_k + s * (K::XB >> 4), yk = y_k + s * (K::YB >> 4);
@@ -294,24 +294,27 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         if (!(ok = wait(&b.full_y[s], ph) && wait(&b.z_full, one) && wait(&b.d_free, one ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int kk = 0; kk < CT / 16; ++kk)   // Zh and Zl are the two panels of one operand of 128 columns
+        for (int kk = 0; kk < CT / 16; ++kk) {   // Zl's tile follows Zh's
             mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk, idD, kk > 0);
+            mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk + (K::ZB >> 4), idD, 1);
+        }
         mma_commit(&b.d_full);
         mma_commit(&b.empty_y[s]);
         if (STATES) continue;
         if (settle(ahead)) issue_pairs(ahead);
-        // O1 takes the half of A that P leaves
-        if (!(ok = ok && wait(&b.s_full, one) && wait(&b.p_full[d], (n >> 1) & 1))) break;
+        if (!(ok = ok && wait(&b.s_full, one))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < DRP / 16; ++kk)
-            mma_bf16(tm + K::T_O1 + d * CT, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
+            mma_bf16(tm + K::T_O1 + d * SL, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
         mma_commit(&b.s_free);
         mma_commit(&b.empty_x[s]);
+        if (!(ok = wait(&b.p_full[d], (n >> 1) & 1) && wait(&b.o_free, one ^ 1))) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)
-            mma_bf16_ts(tm + K::T_O2 + d * SL, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
-        mma_commit(&b.o_full[d]);
+            mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
+        mma_commit(&b.o_full);
         mma_commit(&b.a_free[d]);
     }
     if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
@@ -320,7 +323,67 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     wait(&b.drain, 0);
 }
 
-// ------------------------------------------------------------ warpgroup 1: A -> P
+// ------------------------------------------------------------ warpgroup 1: A -> P, the outputs
+
+// Mild decays keep a part of the pair weights for the outputs (weigh_pairs).
+constexpr float MILD = -2.f;   // log2 of the decay
+// A chunk's outputs, 32 rows a warp: o = f O1 + e O2 with f the power between the state's border and the row, e the row
+// part of the pair weights.
+struct Out {
+    const Pass* p;
+    int row, valid, h, slice;
+    float l2;
+};
+template <int DRP>
+__device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uint32_t n, unsigned char* sm, uint32_t tm, Bars& b) {
+    using K = Cfg<DRP, false>;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, orow = 32 * w + lane;
+    const bool rev = q.p->rev;
+    unsigned char* Ob = sm + K::OFF_O + w * (K::OB / 4);   // this warp's 32 rows
+    const float f = linear::decay_pow(q.l2, rev ? max(0, q.valid - 1 - orow) : orow + 1);
+    const float e = q.l2 >= MILD ? linear::decay_pow(q.l2, rev ? 31 - lane : lane) : 1.f;
+    const uint32_t quarter = (uint32_t)(32 * w) << 16;
+    if (lane == 0) bulk_wait_read();   // the last store has read the staging rows
+    if (!warp_wait(&b.o_full, n & 1)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        float o1[32], o2[32];
+        tmem_ld32(tm + K::T_O1 + (n & 1) * SL + 32 * k + quarter, o1);
+        tmem_ld32(tm + K::T_O2 + 32 * k + quarter, o2);
+        tmem_wait_ld(o1, o2);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float2 v = fma2(make_float2(f, f), make_float2(o1[j], o1[j + 1]), mul2(make_float2(e, e), make_float2(o2[j], o2[j + 1])));
+            o2[j] = v.x;
+            o2[j + 1] = v.y;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) st_row8(Ob, 32, lane, 4 * k + c, o2 + 8 * c);
+    }
+    tc_fence_before();
+    mbar_arrive(&b.o_free);
+    if (q.valid == CT) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&q.p->out, q.slice * SL, q.h, q.row + 32 * w, Ob);
+            bulk_commit();
+        }
+    } else {   // the rows behind the end are not this sequence's: 16-byte pieces of the real ones
+        __syncwarp();
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(q.p->out_ptr);
+#pragma unroll 1
+        for (int x = lane; x < 32 * (SL / 8); x += 32) {
+            const int rr = x / (SL / 8), cc = x % (SL / 8);
+            if (32 * w + rr < q.valid && q.slice * SL + 8 * cc < p.dz)
+                *reinterpret_cast<uint4*>(out + ((size_t)(q.row + 32 * w + rr) * p.seq.H + q.h) * p.dz + q.slice * SL + 8 * cc) =
+                    *reinterpret_cast<const uint4*>(Ob + tile_chunk_off(32, rr, cc));
+        }
+        __syncwarp();
+    }
+    return true;
+}
 
 // Row i = 32 w + lane against column blocks of 32, those on the causal side.
 //
@@ -328,18 +391,18 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
 // to the outputs, the column part 32 |w - jb| -+ j + const between -31 and 96: one value a column for all lanes, read
 // four at a time, and growing to 2^62 at most, which P (8-bit exponents) and the sum take. pw[pos] holds it by position.
 // Stronger decays would overflow it: their weights are read by distance, pw[128 + i - j], 0 off the causal side.
-constexpr float MILD = -2.f;   // log2 of the decay
 template <int DRP>
-__device__ void weigh_pairs(const Params& p, uint32_t tm, Bars& b, float* pw) {
+__device__ void weigh_pairs(const Params& p, unsigned char* sm, uint32_t tm, Bars& b, float* pw) {
     using K = Cfg<DRP, false>;
     const int w = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
     uint32_t n = 0;
     bool ok = true;
+    Out out{};
     for (int x = blockIdx.x; x < p.items; x += gridDim.x) {
         const Item t = item_of<false>(p, x);
         if (t.count() == 0) continue;
         const bool rev = t.p->rev, mild = t.l2 >= MILD;
-        if (named_sync_or(2, 128, !ok)) return;      // the last item's weights have been read
+        if (named_sync_or(2, 128, !ok)) break;       // the last item's weights have been read
         if (mild) {
             pw[rev ? 127 - tid : tid] = exp2f(t.l2 * (float)(96 - tid));
         } else {
@@ -394,11 +457,18 @@ __device__ void weigh_pairs(const Params& p, uint32_t tm, Bars& b, float* pw) {
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&b.p_full[n & 1]);
+            // the chunk before: its O2 ended while this one's P was made
+            if (n > 0 && !(ok = write_outputs<DRP>(p, out, n - 1, sm, tm, b))) break;
+            const int c = t.chunk(i);
+            out = Out{t.p, (int)(t.row0 + (long long)c * CT), t.valid(c), t.h, t.slice, t.l2};
         }
     }
+    if (ok && n > 0) write_outputs<DRP>(p, out, n - 1, sm, tm, b);
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
 }
 
-// ------------------------------------------------------------ warpgroup 2: g_j z_j in two terms, the outputs
+// ------------------------------------------------------------ warpgroup 2: g_j z_j in two terms
 
 // z (gh + gl) as hi + lo, two values at a time in bf16 arithmetic: hi is the rounded product, and its remainder
 // z gh - hi fits bf16 but for its last bit (8 x 8-bit products). The weight, its remainder and lo's rounding leave
@@ -411,70 +481,10 @@ __device__ __forceinline__ void two_terms(uint32_t z2, __nv_bfloat162 gh, __nv_b
     *lo2 = *reinterpret_cast<const uint32_t*>(&lo);
 }
 
-// A chunk's outputs, 32 rows a warp: o = f O1 + e O2 with f the power between the state's border and the row, e the row
-// part of the pair weights (weigh_pairs).
-struct Out {
-    const Pass* p;
-    int row, valid, h, slice;
-    float l2;
-};
-template <int DRP>
-__device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uint32_t n, unsigned char* sm, uint32_t tm, Bars& b) {
-    using K = Cfg<DRP, false>;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, orow = 32 * w + lane;
-    const bool rev = q.p->rev;
-    unsigned char* Ob = sm + K::OFF_O + w * (K::OB / 4);   // this warp's 32 rows
-    const uint32_t d = n & 1;
-    if (!warp_wait(&b.o_full[d], (n >> 1) & 1)) return false;
-    tc_fence_after();
-    if (lane == 0) bulk_wait_read();   // the last store has read them
-    __syncwarp();
-    const float f = linear::decay_pow(q.l2, rev ? max(0, q.valid - 1 - orow) : orow + 1);
-    const float e = q.l2 >= MILD ? linear::decay_pow(q.l2, rev ? 31 - lane : lane) : 1.f;
-    const uint32_t quarter = (uint32_t)(32 * w) << 16;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        float o1[16], o2[16];
-        tmem_ld16(tm + K::T_O1 + d * CT + 16 * k + quarter, o1);
-        tmem_ld16(tm + K::T_O2 + d * SL + 16 * k + quarter, o2);
-        tmem_wait_ld(o1, o2);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float2 v = fma2(make_float2(f, f), make_float2(o1[j], o1[j + 1]), mul2(make_float2(e, e), make_float2(o2[j], o2[j + 1])));
-            o2[j] = v.x;
-            o2[j + 1] = v.y;
-        }
-        st_row8(Ob, 32, lane, 2 * k, o2);
-        st_row8(Ob, 32, lane, 2 * k + 1, o2 + 8);
-    }
-    tc_fence_before();
-    mbar_arrive(&b.o_free[d]);
-    if (q.valid == CT) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d(&q.p->out, q.slice * SL, q.h, q.row + 32 * w, Ob);
-            bulk_commit();
-        }
-    } else {   // the rows behind the end are not this sequence's: 16-byte pieces of the real ones
-        __syncwarp();
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(q.p->out_ptr);
-#pragma unroll 1
-        for (int x = lane; x < 32 * (SL / 8); x += 32) {
-            const int rr = x / (SL / 8), cc = x % (SL / 8);
-            if (32 * w + rr < q.valid && q.slice * SL + 8 * cc < p.dz)
-                *reinterpret_cast<uint4*>(out + ((size_t)(q.row + 32 * w + rr) * p.seq.H + q.h) * p.dz + q.slice * SL + 8 * cc) =
-                    *reinterpret_cast<const uint4*>(Ob + tile_chunk_off(32, rr, cc));
-        }
-        __syncwarp();
-    }
-    return true;
-}
-
 // Z does not come through TMA: its rows go from global memory to registers a chunk ahead (eight lanes a row), and from
 // there to shared memory as they are and as the two terms. Nothing then waits for a stage to be given back.
 template <int DRP, bool STATES>
-__device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t tm, Bars& b) {
+__device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
     const int r0 = 32 * w + (lane >> 3), c = lane & 7;   // rows r0 + 4 k, 16-byte piece c
@@ -504,8 +514,6 @@ __device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t 
     if (more) load();
     __nv_bfloat162 gh[8], gl[8];   // the rows' weights
     int have = -1, have_x = -1;
-    Out out{};   // of the chunk before: its outputs are written once this one's values are on their way
-    bool ok = true;
     while (more) {
         const int valid = t.valid(t.chunk(i));
         const float l2 = t.l2;
@@ -524,12 +532,11 @@ __device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t 
         uint4 z[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) z[k] = ahead[k];
-        const Out mine{t.p, (int)(t.row0 + (long long)t.chunk(i) * CT), valid, t.h, t.slice, l2};
         more = next();
         if (more) load();
         // Zh and Zl are free once the last chunk's D is done, this copy of Z once the chunk before that has its O2
-        if (!(ok = n == 0 || warp_wait(&b.d_full, (n - 1) & 1))) break;
-        if (!STATES && !(ok = warp_wait(&b.a_free[n & 1], ((n >> 1) & 1) ^ 1))) break;
+        if (n > 0 && !warp_wait(&b.d_full, (n - 1) & 1)) return;
+        if (!STATES && !warp_wait(&b.a_free[n & 1], ((n >> 1) & 1) ^ 1)) return;
         unsigned char* Z = sm + K::OFF_Z + (n & 1) * K::ZB;
         unsigned char *Zh = sm + K::OFF_ZH, *Zl = sm + K::OFF_ZL;
 #pragma unroll
@@ -546,7 +553,7 @@ __device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t 
         }
         if (valid < CT) {   // rows of Y behind the sequence's end: they are another's, and would meet the zeros of Z
             const uint32_t s = n % K::STAGES;
-            if (!(ok = warp_wait(&b.full_y[s], (n / K::STAGES) & 1))) break;
+            if (!warp_wait(&b.full_y[s], (n / K::STAGES) & 1)) return;
             if (tid >= valid)
 #pragma unroll 1
                 for (int q = 0; q < DRP / 8; ++q)
@@ -554,14 +561,8 @@ __device__ void values_and_outputs(const Params& p, unsigned char* sm, uint32_t 
         }
         fence_async_smem();
         mbar_arrive(&b.z_full);
-        if (!STATES && n > 0 && !(ok = write_outputs<DRP>(p, out, n - 1, sm, tm, b))) break;
-        out = mine;
         ++n;
     }
-    if (STATES) return;
-    if (ok && n > 0) write_outputs<DRP>(p, out, n - 1, sm, tm, b);
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
 }
 
 // ------------------------------------------------------------ warpgroup 3: the state
@@ -640,25 +641,23 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
                 tc_fence_after();
                 const float aC = linear::decay_pow(t.l2, valid);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float hi[16], lo[16];
-                    tmem_ld16(tm + K::T_D + 16 * h + quarter, hi);
-                    tmem_ld16(tm + K::T_D + SL + 16 * h + quarter, lo);
-                    tmem_wait_ld(hi, lo);
+                for (int h = 0; h < 2; ++h) {
+                    float D[32];
+                    tmem_ld32(tm + K::T_D + 32 * h + quarter, D);
+                    tmem_wait_ld(D);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float2 v = fma2(make_float2(aC, aC), make_float2(S[16 * h + j], S[16 * h + j + 1]),
-                                              add2(make_float2(hi[j], hi[j + 1]), make_float2(lo[j], lo[j + 1])));
-                        S[16 * h + j] = v.x;
-                        S[16 * h + j + 1] = v.y;
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 v = fma2(make_float2(aC, aC), make_float2(S[32 * h + j], S[32 * h + j + 1]), make_float2(D[j], D[j + 1]));
+                        S[32 * h + j] = v.x;
+                        S[32 * h + j + 1] = v.y;
                     }
                 }
                 tc_fence_before();
                 mbar_arrive(&b.d_free);
-                if (!STATES && i + 1 < t.count()) {
-                    ok = warp_wait(&b.s_free, n & 1);
-                    if (ok) copy_state();
-                }
+            }
+            if (!STATES && ok && i + 1 < t.count()) {
+                ok = warp_wait(&b.s_free, n & 1);
+                if (ok) copy_state();
             }
             if (!ok) break;
         }
@@ -692,9 +691,9 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.a_full[i], 1); mbar_init(&b.a_free[i], 1); mbar_init(&b.p_full[i], 128);
-            mbar_init(&b.o_full[i], 1); mbar_init(&b.o_free[i], 128);
         }
         mbar_init(&b.z_full, 128);
+        mbar_init(&b.o_full, 1); mbar_init(&b.o_free, 128);
         mbar_init(&b.d_full, 1); mbar_init(&b.d_free, 128);
         mbar_init(&b.s_full, 128); mbar_init(&b.s_free, 1);
         mbar_init(&b.drain, 1);
@@ -715,8 +714,8 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
         if (elect_one()) issue_products<DRP, STATES>(p, sm, tm, b);
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
-        if constexpr (!STATES) weigh_pairs<DRP>(p, tm, b, pw);
-    } else if (warp >= 8 && warp < 12) values_and_outputs<DRP, STATES>(p, sm, tm, b);
+        if constexpr (!STATES) weigh_pairs<DRP>(p, sm, tm, b, pw);
+    } else if (warp >= 8 && warp < 12) split_values<DRP, STATES>(p, sm, b);
     else if (warp >= 12) carry_state<DRP, STATES>(p, sm, tm, b);
     tc_fence_before();
     __syncthreads();
