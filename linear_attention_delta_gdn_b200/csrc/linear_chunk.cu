@@ -98,8 +98,15 @@ __device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
     }
     t->l2 = linear::log2_decay(p.log_decay, t->h);
 }
+// The block's first item is found once, before the roles start (its loads and the first reads of the parameters take as
+// long as a chunk).
+__device__ __forceinline__ Item& first_item() {
+    __shared__ Item first;
+    return first;
+}
 template <bool STATES>
 __device__ __forceinline__ Item item_of(const Params& p, int x) {
+    if (x == (int)blockIdx.x) return first_item();
     Item t;
     find_item<STATES>(p, (uint32_t)x, &t);
     return t;
@@ -122,7 +129,7 @@ struct Cfg {
 };
 
 struct Bars {
-    uint64_t full_x[4], full_y[4], empty_x[4], empty_y[4];
+    uint64_t full[4], empty_x[4], empty_y[4];
     uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full, o_free, drain;
 };
 
@@ -157,6 +164,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t phase) {
     const uint32_t addr = smem_u32(bar);
     return try_wait(addr, phase) || wait_on(addr, phase);
 }
+// Two barriers whose tries are on their way together.
+__device__ __forceinline__ bool wait2(uint64_t* bar0, uint32_t phase0, uint64_t* bar1, uint32_t phase1) {
+    const uint32_t a0 = smem_u32(bar0), a1 = smem_u32(bar1);
+    const bool r0 = try_wait(a0, phase0), r1 = try_wait(a1, phase1);
+    return (r0 || wait_on(a0, phase0)) && (r1 || wait_on(a1, phase1));
+}
 // A whole warp: one lane asks (a dozen warps asking with every lane get in each other's way), all have its answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
     bool ok = true;
@@ -175,13 +188,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
         : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
     return r;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-    return r;
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
@@ -196,7 +202,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 template <int DRP, bool STATES>
 __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
-    uint32_t ny = 0, nx = 0;   // tiles asked for so far, over all items
+    uint32_t ny = 0;   // stages asked for so far, over all items
     bool ok = true;
     for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
         const Item t = item_of<STATES>(p, it);
@@ -204,30 +210,26 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
             const uint32_t s = ny % K::STAGES, ph = ((ny / K::STAGES) & 1) ^ 1;
             const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
             if (!(ok = wait(&b.empty_y[s], ph))) break;
-            mbar_arrive_expect_tx(&b.full_y[s], K::YB);
+            mbar_arrive_expect_tx(&b.full[s], K::YB);
 #pragma unroll
             for (int c = 0; c < DRP / 64; ++c)
-                tma_load_3d(sm + K::OFF_Y + s * K::YB + c * CT * 128, &t.p->y, 64 * c, t.h, row, &b.full_y[s]);
+                tma_load_3d(sm + K::OFF_Y + s * K::YB + c * CT * 128, &t.p->y, 64 * c, t.h, row, &b.full[s]);
             ++ny;
-            if (!STATES) {
+            if (!STATES) {   // X and Y come back at different times, and are waited for together
                 if (!(ok = wait(&b.empty_x[s], ph))) break;
-                mbar_arrive_expect_tx(&b.full_x[s], K::XB);
+                mbar_arrive_expect_tx(&b.full[s], K::XB);
 #pragma unroll
                 for (int c = 0; c < DRP / 64; ++c)
-                    tma_load_3d(sm + s * K::XB + c * CT * 128, &t.p->x, 64 * c, t.h, row, &b.full_x[s]);
-                ++nx;
+                    tma_load_3d(sm + s * K::XB + c * CT * 128, &t.p->x, 64 * c, t.h, row, &b.full[s]);
             }
         }
     }
     if (ok) return;   // every tile was waited for by those who read it
     atomicOr(&g_linear_error, linear::ERR_WAIT);
-    // let the copies in flight land before the block gives up its shared memory: each stage's last one
-    auto land = [](uint64_t* full, uint32_t asked) {
-        for (uint32_t k = 1; k <= (uint32_t)K::STAGES && k <= asked; ++k)
-            wait(&full[(asked - k) % K::STAGES], ((asked - k) / K::STAGES) & 1);
-    };
-    land(b.full_y, ny);
-    land(b.full_x, nx);
+    // let the copies in flight land before the block gives up its shared memory: each stage's last ones. A stage whose X
+    // was not asked for any more keeps its barrier open; its Y has the time that wait takes.
+    for (uint32_t k = 1; k <= (uint32_t)K::STAGES && k <= ny; ++k)
+        wait(&b.full[(ny - k) % K::STAGES], ((ny - k) / K::STAGES) & 1);
 }
 
 // ------------------------------------------------------------ warp 1: products
@@ -271,8 +273,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         const uint32_t n = c.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, dph = (n >> 1) & 1;
         const bool ragged = c.ragged_end && c.i == (c.rev ? 0 : c.count - 1);
         // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
-        ok = wait(&b.full_y[s], ph) && (!ragged || wait(&b.z_full, n & 1)) && wait(&b.full_x[s], ph) &&
-             wait(&b.a_free[d], dph ^ 1);
+        ok = wait2(&b.full[s], ph, &b.a_free[d], dph ^ 1) && (!ragged || wait(&b.z_full, n & 1));
         if (!ok) return;
         tc_fence_after();
         const uint64_t xk = x_k + s * (K::XB >> 4), yk = y_k + s * (K::YB >> 4);
@@ -291,7 +292,8 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         const uint64_t xk = x_k + s * (K::XB >> 4), ymn = y_mn + s * (K::YB >> 4), zmn = z_mn + d * (K::ZB >> 4);
         ++cur.i;
         ++cur.n;
-        if (!(ok = wait(&b.full_y[s], ph) && wait(&b.z_full, one) && wait(&b.d_free, one ^ 1))) break;
+        if (STATES && !(ok = wait(&b.full[s], ph))) break;   // else A has waited for it
+        if (!(ok = wait2(&b.z_full, one, &b.d_free, one ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk) {   // Zl's tile follows Zh's
@@ -309,7 +311,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
             mma_bf16(tm + K::T_O1 + d * SL, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
         mma_commit(&b.s_free);
         mma_commit(&b.empty_x[s]);
-        if (!(ok = wait(&b.p_full[d], (n >> 1) & 1) && wait(&b.o_free, one ^ 1))) break;
+        if (!(ok = wait2(&b.p_full[d], (n >> 1) & 1, &b.o_free, one ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)
@@ -553,7 +555,7 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
         }
         if (valid < CT) {   // rows of Y behind the sequence's end: they are another's, and would meet the zeros of Z
             const uint32_t s = n % K::STAGES;
-            if (!warp_wait(&b.full_y[s], (n / K::STAGES) & 1)) return;
+            if (!warp_wait(&b.full[s], (n / K::STAGES) & 1)) return;
             if (tid >= valid)
 #pragma unroll 1
                 for (int q = 0; q < DRP / 8; ++q)
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int s = 0; s < K::STAGES; ++s) {
-            mbar_init(&b.full_x[s], 1); mbar_init(&b.full_y[s], 1);
+            mbar_init(&b.full[s], STATES ? 1 : 2);
             mbar_init(&b.empty_x[s], 1); mbar_init(&b.empty_y[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -702,6 +704,12 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     if (warp == 2) {
         tmem_alloc(&tmem, 512);
         tmem_relinquish();
+    }
+    if (threadIdx.x == 96) {
+        find_item<STATES>(p, blockIdx.x, &first_item());
+        if (!STATES) tma_prefetch_desc(&first_item().p->x);
+        tma_prefetch_desc(&first_item().p->y);
+        if (!STATES) tma_prefetch_desc(&first_item().p->out);
     }
     tc_fence_before();
     __syncthreads();
