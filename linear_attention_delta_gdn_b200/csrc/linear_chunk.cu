@@ -5,7 +5,7 @@
 //     out = diag(f) X R + P Z,        R' = a^C R + Y^T diag(g) Z
 // A block owns 64 columns of Z (and of out and R), so a head of 128 is two blocks and 64 heads fill the GPU; X and Y
 // are then read by both, the second time from L2. Products per chunk and block (tcgen05, M = 128, 32-bit TMEM):
-//     A = X Y^T (N 128)    D = Y^T Zh + Y^T Zl (N 64)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
+//     A = X Y^T (N 128)    D = Y^T [Zh | Zl] (N 128)    O1 = X R (N 64)    O2 = P Z (N 64, P read from TMEM)
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
@@ -46,7 +46,7 @@ constexpr int NT = 512;         // threads of a block
 constexpr int MAX_PASS = 3;
 
 struct Pass {
-    CUtensorMap x, y, out;
+    CUtensorMap x, y, z, out;
     const void* z_ptr;
     const float* start;      // state in front of the first (behind the last) token, [N, H, Dk, Dv], or null
     float* end;              // the state at the other end, or null
@@ -124,8 +124,8 @@ struct Cfg {
     static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + ZRAW * ZB,
                               OFF_ZL = OFF_ZH + ZB, OFF_S = OFF_ZL + ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
     static constexpr uint32_t SMEM = TOTAL + 1024;                 // tiles start on 1024 bytes
-    // TMEM columns: A twice (then P in its first half), D, O1 twice, O2
-    static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 320, T_O2 = 448;
+    // TMEM columns: A twice (then P in its first half), D (its Zh and its Zl part), O1, O2
+    static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 384, T_O2 = 448;
 };
 
 struct Bars {
@@ -204,10 +204,24 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     using K = Cfg<DRP, STATES>;
     uint32_t ny = 0;   // stages asked for so far, over all items
     bool ok = true;
+    // Two stages of X and Y cover the time of a read from L2, not that of one from memory: what comes AHEAD chunks later
+    // is brought into L2 meanwhile, X and Y by one of a head's slices each.
+    constexpr int AHEAD = 3;
+    auto into_l2 = [&](const Item& t, int i) {
+        const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
+#pragma unroll 1
+        for (int c = 0; c < DRP / 64; ++c) {
+            if (!STATES && t.slice == 0) tma_prefetch_3d(&t.p->x, 64 * c, t.h, row);
+            if (t.slice == p.slices - 1) tma_prefetch_3d(&t.p->y, 64 * c, t.h, row);
+        }
+        tma_prefetch_3d(&t.p->z, t.slice * SL, t.h, row);
+    };
     for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
         const Item t = item_of<STATES>(p, it);
+        for (int i = 1; i < AHEAD && i < t.count(); ++i) into_l2(t, i);
         for (int i = 0; i < t.count(); ++i) {
             const uint32_t s = ny % K::STAGES, ph = ((ny / K::STAGES) & 1) ^ 1;
+            if (i + AHEAD < t.count()) into_l2(t, i + AHEAD);
             const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
             if (!(ok = wait(&b.empty_y[s], ph))) break;
             mbar_arrive_expect_tx(&b.full[s], K::YB);
@@ -243,7 +257,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     const uint64_t x_k = desc_k(base, CT, 0, 0), y_k = desc_k(base + K::OFF_Y, CT, 0, 0),
                    y_mn = desc_mn(base + K::OFF_Y, CT, 0, 0), z_mn = desc_mn(base + K::OFF_Z, CT, 0, 0),
                    zh_mn = desc_mn(base + K::OFF_ZH, CT, 0, 0), s_mn = desc_mn(base + K::OFF_S, DRP, 0, 0);
-    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, SL, true, true),
+    const uint32_t idA = idesc_bf16(128, 128, false, false), idD = idesc_bf16(DRP, 2 * SL, true, true),
                    idO = idesc_bf16(128, SL, false, true);
     constexpr uint64_t MN = (16 * 128) >> 4;   // 16 rows of an MN-major tile
     // K-major: 32 bytes a step within a panel of 64 columns, then the next panel
@@ -296,22 +310,20 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         if (!(ok = wait2(&b.z_full, one, &b.d_free, one ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int kk = 0; kk < CT / 16; ++kk) {   // Zl's tile follows Zh's
+        for (int kk = 0; kk < CT / 16; ++kk)   // Zh and Zl are the two panels of one operand of 128 columns: Y is read once
             mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk, idD, kk > 0);
-            mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk + (K::ZB >> 4), idD, 1);
-        }
         mma_commit(&b.d_full);
         mma_commit(&b.empty_y[s]);
         if (STATES) continue;
         if (settle(ahead)) issue_pairs(ahead);
-        if (!(ok = ok && wait(&b.s_full, one))) break;
+        if (!(ok = ok && wait2(&b.s_full, one, &b.o_free, one ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < DRP / 16; ++kk)
-            mma_bf16(tm + K::T_O1 + d * SL, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
+            mma_bf16(tm + K::T_O1, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
         mma_commit(&b.s_free);
         mma_commit(&b.empty_x[s]);
-        if (!(ok = wait2(&b.p_full[d], (n >> 1) & 1, &b.o_free, one ^ 1))) break;
+        if (!(ok = wait(&b.p_full[d], (n >> 1) & 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)
@@ -351,7 +363,7 @@ __device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uin
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         float o1[32], o2[32];
-        tmem_ld32(tm + K::T_O1 + (n & 1) * SL + 32 * k + quarter, o1);
+        tmem_ld32(tm + K::T_O1 + 32 * k + quarter, o1);
         tmem_ld32(tm + K::T_O2 + 32 * k + quarter, o2);
         tmem_wait_ld(o1, o2);
 #pragma unroll
@@ -643,15 +655,17 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
                 tc_fence_after();
                 const float aC = linear::decay_pow(t.l2, valid);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float D[32];
-                    tmem_ld32(tm + K::T_D + 32 * h + quarter, D);
-                    tmem_wait_ld(D);
+                for (int h = 0; h < 4; ++h) {
+                    float hi[16], lo[16];
+                    tmem_ld16(tm + K::T_D + 16 * h + quarter, hi);
+                    tmem_ld16(tm + K::T_D + SL + 16 * h + quarter, lo);
+                    tmem_wait_ld(hi, lo);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 v = fma2(make_float2(aC, aC), make_float2(S[32 * h + j], S[32 * h + j + 1]), make_float2(D[j], D[j + 1]));
-                        S[32 * h + j] = v.x;
-                        S[32 * h + j + 1] = v.y;
+                    for (int j = 0; j < 16; j += 2) {   // a^C S, then the small part, then the large one
+                        const float2 v = fma2(make_float2(aC, aC), make_float2(S[16 * h + j], S[16 * h + j + 1]),
+                                              make_float2(lo[j], lo[j + 1]));
+                        S[16 * h + j] = v.x + hi[j];
+                        S[16 * h + j + 1] = v.y + hi[j + 1];
                     }
                 }
                 tc_fence_before();
@@ -873,7 +887,7 @@ cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
                     bool transposed, bool rev) {
         Pass p{};
         good = good && encode(&p.x, x, q, dr, CT) == CUDA_SUCCESS && encode(&p.y, y, q, dr, CT) == CUDA_SUCCESS &&
-               encode(&p.out, out, q, dz, 32) == CUDA_SUCCESS;
+               encode(&p.z, z, q, dz, CT) == CUDA_SUCCESS && encode(&p.out, out, q, dz, 32) == CUDA_SUCCESS;
         p.start = start;
         p.end = end;
         p.seg = seg(dr, dz);
