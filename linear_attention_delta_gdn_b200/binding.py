@@ -439,29 +439,24 @@ def _on(t: torch.Tensor, device, name: str):
 def _opt(t: Optional[torch.Tensor], device, name: str, dtype, shape):
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError("%s must be %s %s" % (name, dtype, list(shape)))
     return _on(t, device, name)
 
 
-class _Device:
-    """The call's device made current (launches go to the current device) and its current stream."""
+# the current stream's handle without the Stream object around it, which costs more than a launch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
-    def __init__(self, t: torch.Tensor):
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        self.device = t.device
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _here(t: torch.Tensor, call):
+    """``call(device, stream)`` with t's device current (launches go to the current device) and its current stream."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    dev = t.device
+    if dev.index == torch.cuda.current_device():
+        return call(dev, _raw_stream(dev.index))
+    with torch.cuda.device(dev):
+        return call(dev, _raw_stream(dev.index))
 
 
 def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int, dt: int) -> int:
@@ -471,16 +466,18 @@ def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int
 def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs, ends):
     """Shared by the four whole-sequence calls: checks, outputs, workspace, the call. Returns (outs, end state)."""
     packed = cu is not None
-    lead = tuple(q.shape[:-2])
     if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
         raise ValueError("q and v must be [%sH, D]" % ("Ttot, " if packed else "B, T, "))
-    H, Dk = q.shape[-2:]
+    *lead, H, Dk = q.shape
     Dv = v.shape[-1]
-    dev, dt, code = q.device, q.dtype, _dt(q)
-    for name, t, D in (("k", k, Dk), ("v", v, Dv)) + ((("dout", dout, Dv),) if dout is not None else ()):
-        if t.dtype != dt or tuple(t.shape) != lead + (H, D):
-            raise ValueError("%s must be %s %s" % (name, dt, list(lead + (H, D))))
-    if log_decay.dtype != torch.float32 or tuple(log_decay.shape) != (H,):
+    dt, code = q.dtype, _dt(q)
+    if k.dtype != dt or k.shape != q.shape:
+        raise ValueError("k must be %s %s" % (dt, list(q.shape)))
+    if v.dtype != dt or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError("v must be %s %s" % (dt, lead + [H, "Dv"]))
+    if dout is not None and (dout.dtype != dt or dout.shape != v.shape):
+        raise ValueError("dout must be %s %s" % (dt, list(v.shape)))
+    if log_decay.dtype != torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != H:
         raise ValueError("log_decay must be float32 [%d]" % H)
     if packed:
         if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:
@@ -490,7 +487,10 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
         N, T = lead
     bwd = dout is not None
     state = (N, H, Dk, Dv)
-    with _Device(q) as stream:
+    f32 = torch.float32
+
+    def call(dev, stream):
+        nonlocal ws
         made = []
         for name, t, like in outs:
             if t is None:
@@ -500,11 +500,11 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
             made.append(t)
         name, end = ends
         if end is None and want_end:
-            end = torch.empty(state, dtype=torch.float32, device=dev)
-        need = lib().gdn2_linear_workspace_size(GDN2_OP_BWD if bwd else GDN2_OP_FWD, N, T, H, Dk, Dv, code)
+            end = q.new_empty(state, dtype=f32)
+        L = lib()
+        need = L.gdn2_linear_workspace_size(GDN2_OP_BWD if bwd else GDN2_OP_FWD, N, T, H, Dk, Dv, code)
         if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        f32 = torch.float32
+            ws = q.new_empty(need, dtype=torch.uint8)
         args = [_on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay")]
         if packed:
             args += [_on(cu, dev, "cu_seqlens"), N, T, lead[0]]
@@ -515,10 +515,13 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
         args.append(_opt(end, dev, name, f32, state))
         if not packed:
             args += [N, T]
-        rc = getattr(lib(), fn)(*args, H, Dk, Dv, code, None if ws is None else _on(ws, dev, "ws"),
-                                0 if ws is None else ws.numel() * ws.element_size(), stream)
-    _check(fn, rc)
-    return made, end
+        rc = getattr(L, fn)(*args, H, Dk, Dv, code, None if ws is None else _on(ws, dev, "ws"),
+                            0 if ws is None else ws.numel() * ws.element_size(), stream)
+        if rc:
+            _check(fn, rc)
+        return made, end
+
+    return _here(q, call)
 
 
 def gdn2_linear_fwd(q, k, v, log_decay, S0=None, want_state: bool = True, ws: Optional[torch.Tensor] = None, o=None, ST=None):
@@ -571,24 +574,26 @@ def gdn2_linear_decode_step(q, k, v, log_decay, S, slots=None, o=None):
         raise ValueError("q and v must be [B, H, D]")
     B, H, Dk = q.shape
     Dv = v.shape[-1]
-    dev, dt, code = q.device, q.dtype, _dt(q)
+    dt, code = q.dtype, _dt(q)
     if k.dtype != dt or k.shape != q.shape or v.dtype != dt or v.shape[:2] != q.shape[:2]:
         raise ValueError("k and v must be %s [%d, %d, D]" % (dt, B, H))
     if log_decay.dtype != torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != H:
         raise ValueError("log_decay must be float32 [%d]" % H)
-    if S.dtype != torch.float32 or S.dim() != 4 or tuple(S.shape[1:]) != (H, Dk, Dv):
+    if S.dtype != torch.float32 or S.dim() != 4 or S.shape[1:] != (H, Dk, Dv):
         raise ValueError("S must be float32 [num_slots, %d, %d, %d]" % (H, Dk, Dv))
-    with _Device(q) as stream:
-        if o is None:
-            o = torch.empty((B, H, Dv), dtype=dt, device=dev)
-        elif o.dtype != dt or tuple(o.shape) != (B, H, Dv):
-            raise ValueError("o must be %s [%d, %d, %d]" % (dt, B, H, Dv))
+    if o is not None and (o.dtype != dt or o.shape != v.shape):
+        raise ValueError("o must be %s [%d, %d, %d]" % (dt, B, H, Dv))
+
+    def call(dev, stream):
+        out = torch.empty_like(v, memory_format=torch.contiguous_format) if o is None else o
         rc = lib().gdn2_linear_decode_step(
             _on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay"), _on(S, dev, "S"),
-            None if slots is None else _opt(slots, dev, "slots", torch.int32, (B,)), S.shape[0], _on(o, dev, "o"),
-            B, H, Dk, Dv, code, stream)
-    _check("gdn2_linear_decode_step", rc)
-    return o
+            _opt(slots, dev, "slots", torch.int32, (B,)), S.shape[0], _on(out, dev, "o"), B, H, Dk, Dv, code, stream)
+        if rc:
+            _check("gdn2_linear_decode_step", rc)
+        return out
+
+    return _here(q, call)
 
 
 class DecayLinearAttention(torch.autograd.Function):
@@ -641,9 +646,10 @@ def rope_axes(sections, device="cuda") -> torch.Tensor:
 
 def _rows_of(t, name, B, T, H, D):
     """Pointer and token stride of [B, T, H, D] whose heads are contiguous and whose tokens are evenly spaced."""
-    if t.stride(3) != 1 and D > 1 or t.stride(2) != D and H > 1 or (B > 1 and T > 1 and t.stride(0) != T * t.stride(1)):
+    sb, st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1) or (B > 1 and T > 1 and sb != T * st):
         raise ValueError("%s: a token's heads must be contiguous and the tokens evenly spaced" % name)
-    return t.data_ptr(), (t.stride(1) if T > 1 else t.stride(0) if B > 1 else H * D)
+    return t.data_ptr(), (st if T > 1 else sb if B > 1 else H * D)
 
 
 def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved):
@@ -657,12 +663,12 @@ def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
         raise ValueError("q and k must be of one dtype and on one device")
     if positions.dtype not in (torch.int32, torch.int64):
         raise TypeError("positions must be int32 or int64")
-    if positions.dim() not in (2, 3) or tuple(positions.shape[-2:]) != (B, T):
+    if positions.dim() not in (2, 3) or positions.shape[-2:] != (B, T):
         raise ValueError("positions must be [B, T] or [axes, B, T] = [..., %d, %d]" % (B, T))
     num_axes = positions.shape[0] if positions.dim() == 3 else 1
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be float32 [pairs]")
-    P = inv_freq.numel()
+    P = inv_freq.shape[0]
     if num_axes > 1 and axes is None:
         raise ValueError("positions of several axes need axes, the axis of each pair")
     norm = eps is not None
@@ -672,7 +678,7 @@ def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
     qp, qs = _rows_of(q, "q", B, T, Hq, D)
     kp, ks = _rows_of(k, "k", B, T, Hk, D)
     tail = (_on(positions, dev, "positions"), positions.element_size(), num_axes, _on(inv_freq, dev, "inv_freq"),
-            _opt(axes, dev, "axes", torch.int32, (P,)), P, int(interleaved), int(norm), eps if norm else 0.0,
+            _opt(axes, dev, "axes", torch.int32, (P,)), P, 1 if interleaved else 0, 1 if norm else 0, eps if norm else 0.0,
             _opt(q_weight, dev, "q_weight", f32, (D,)), _opt(k_weight, dev, "k_weight", f32, (D,)))
     return (B, T, Hq, Hk, D, _dt(q)), (qp, kp, qs, ks), tail
 
@@ -686,37 +692,42 @@ def gdn2_qk_norm_rope_fwd(q, k, positions, inv_freq, axes=None, q_weight=None, k
     :func:`rope_axes`) naming each pair's axis, inv_freq fp32 [pairs], weights fp32 [D] or None. ``eps=None``: no norm.
     Pairs are channels (p, p + pairs), or (2p, 2p + 1) if ``interleaved``. Returns ``(q_out, k_out)``, contiguous.
     """
-    with _Device(q) as stream:
+    def call(dev, stream):
         sizes, lead, tail = _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        rc = lib().gdn2_qk_norm_rope_fwd(*lead, *tail, _opt(q_out, q.device, "q_out", q.dtype, tuple(q.shape)),
-                                         _opt(k_out, q.device, "k_out", q.dtype, tuple(k.shape)), *sizes, stream)
-    _check("gdn2_qk_norm_rope_fwd", rc)
-    return q_out, k_out
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        ko = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
+        rc = lib().gdn2_qk_norm_rope_fwd(*lead, *tail, _opt(qo, dev, "q_out", q.dtype, q.shape),
+                                         _opt(ko, dev, "k_out", q.dtype, k.shape), *sizes, stream)
+        if rc:
+            _check("gdn2_qk_norm_rope_fwd", rc)
+        return qo, ko
+
+    return _here(q, call)
 
 
 def gdn2_qk_norm_rope_bwd(q, k, dq_out, dk_out, positions, inv_freq, axes=None, q_weight=None, k_weight=None,
                           eps: Optional[float] = 1e-6, interleaved: bool = False, ws: Optional[torch.Tensor] = None):
     """Backward of :func:`gdn2_qk_norm_rope_fwd`: dict with dq, dk and, for given weights, dq_weight, dk_weight (fp32;
     None otherwise)."""
-    with _Device(q) as stream:
+    def call(dev, stream):
+        nonlocal ws
         sizes, lead, tail = _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
-        dev, D = q.device, q.shape[3]
-        g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=k.dtype, device=dev),
-             "dq_weight": None if q_weight is None else torch.empty(D, dtype=torch.float32, device=dev),
-             "dk_weight": None if k_weight is None else torch.empty(D, dtype=torch.float32, device=dev)}
+        D, dt = q.shape[3], q.dtype
+        g = {"dq": torch.empty_like(q, memory_format=torch.contiguous_format),
+             "dk": torch.empty_like(k, memory_format=torch.contiguous_format),
+             "dq_weight": None if q_weight is None else torch.empty_like(q_weight),
+             "dk_weight": None if k_weight is None else torch.empty_like(k_weight)}
         if ws is None and (q_weight is not None or k_weight is not None):
-            ws = torch.empty(lib().gdn2_qk_norm_rope_workspace_size(D), dtype=torch.uint8, device=dev)
+            ws = q.new_empty(lib().gdn2_qk_norm_rope_workspace_size(D), dtype=torch.uint8)
         rc = lib().gdn2_qk_norm_rope_bwd(
-            *lead, _opt(dq_out, dev, "dq_out", q.dtype, tuple(q.shape)), _opt(dk_out, dev, "dk_out", q.dtype, tuple(k.shape)),
-            *tail, g["dq"].data_ptr(), g["dk"].data_ptr(),
-            *(None if g[n] is None else g[n].data_ptr() for n in ("dq_weight", "dk_weight")), *sizes,
-            None if ws is None else _on(ws, dev, "ws"), 0 if ws is None else ws.numel() * ws.element_size(), stream)
-    _check("gdn2_qk_norm_rope_bwd", rc)
-    return g
+            *lead, _opt(dq_out, dev, "dq_out", dt, q.shape), _opt(dk_out, dev, "dk_out", dt, k.shape), *tail,
+            g["dq"].data_ptr(), g["dk"].data_ptr(), *(None if g[n] is None else g[n].data_ptr() for n in ("dq_weight", "dk_weight")),
+            *sizes, None if ws is None else _on(ws, dev, "ws"), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+        if rc:
+            _check("gdn2_qk_norm_rope_bwd", rc)
+        return g
+
+    return _here(q, call)
 
 
 class QkNormRope(torch.autograd.Function):
