@@ -169,7 +169,7 @@ gdn2_status gdn2_linear_decode_step(const void* q, const void* k, const void* v,
     return cuda_status(linear_step_launch(a, static_cast<cudaStream_t>(stream)), "gdn2_linear_decode_step");
 }
 
-size_t gdn2_qk_norm_rope_workspace_size(int D) { return dim_ok(D) ? (size_t)QK_ROPE_BLOCKS * 2 * D * sizeof(float) : 0; }
+size_t gdn2_qk_norm_rope_workspace_size(int D) { return dim_ok(D) ? (size_t)QK_ROPE_BLOCKS * D * sizeof(float) : 0; }
 
 static gdn2_status rope(QkRopeArgs a, int pos_bytes, int B, int T, bool bwd, void* ws, size_t ws_bytes, void* stream,
                         const char* fn) {

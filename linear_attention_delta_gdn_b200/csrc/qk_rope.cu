@@ -9,7 +9,8 @@
 //
 // The rows are read and written once (HBM-bound). An angle is the same for all heads of a token: a warp takes a token,
 // makes its cosines and sines once, each lane keeps those of its channels in registers, and the token's rows pass by,
-// several in flight, 16 bytes a lane at each of a pair's two places. Few tokens: several warps share a token's heads.
+// several in flight as they lie in memory, 16 bytes a lane at each of a pair's two places. What an angle needs 64 bits
+// for does not depend on the token and is made once a block. Few tokens: several warps share a token's heads.
 // Far positions: the angle is a whole-number product modulo one turn, so a position of millions (or of 2^40) keeps the
 // error of a small one (a 32-bit product is off by 0.06 at a million).
 #include <cuda_bf16.h>
@@ -21,62 +22,45 @@
 namespace gdn2 {
 namespace {
 
-constexpr int WARPS = 4;           // warps of a block, one token each
+constexpr int WARPS = 8;           // warps of a block, each with tokens of its own
 
 __device__ unsigned int g_rope_error;
 
-// VEC consecutive channels at each of a pair's two places; interleaved pairs lie next to one another.
-template <int VEC>
-__device__ __forceinline__ void get(const float* p, float* x) {
-    if constexpr (VEC >= 4) {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(p + i);
-            x[i] = u.x; x[i + 1] = u.y; x[i + 2] = u.z; x[i + 3] = u.w;
-        }
-    } else {
-        x[0] = *p;
-    }
-}
-__device__ __forceinline__ void unpack(uint32_t u, float* x) {
+// VEC consecutive channels as they lie in memory, and as floats.
+template <int BYTES> struct Piece;
+template <> struct Piece<16> { using type = uint4; };
+template <> struct Piece<8> { using type = uint2; };
+template <> struct Piece<4> { using type = uint32_t; };
+template <> struct Piece<2> { using type = unsigned short; };
+template <typename T, int VEC>
+using piece_t = typename Piece<VEC * (int)sizeof(T)>::type;
+
+__device__ __forceinline__ void widen(uint32_t u, float* x) {
     x[0] = __uint_as_float(u << 16);
     x[1] = __uint_as_float(u & 0xffff0000u);
 }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
+__device__ __forceinline__ uint32_t narrow(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-template <int VEC>
-__device__ __forceinline__ void get(const __nv_bfloat16* p, float* x) {
-    if constexpr (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        unpack(u.x, x); unpack(u.y, x + 2); unpack(u.z, x + 4); unpack(u.w, x + 6);
-    } else if constexpr (VEC == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        unpack(u.x, x); unpack(u.y, x + 2);
-    } else {
-        x[0] = __bfloat162float(*p);
-    }
+__device__ __forceinline__ void widen(const uint4& u, float (&x)[8], __nv_bfloat16) {
+    widen(u.x, x); widen(u.y, x + 2); widen(u.z, x + 4); widen(u.w, x + 6);
 }
-template <int VEC>
-__device__ __forceinline__ void put(float* p, const float* x) {
-    if constexpr (VEC >= 4) {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-    } else {
-        *p = x[0];
-    }
+__device__ __forceinline__ void widen(const uint2& u, float (&x)[4], __nv_bfloat16) { widen(u.x, x); widen(u.y, x + 2); }
+__device__ __forceinline__ void widen(unsigned short u, float (&x)[1], __nv_bfloat16) { x[0] = __uint_as_float((uint32_t)u << 16); }
+__device__ __forceinline__ void widen(const uint4& u, float (&x)[4], float) {
+    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y); x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
 }
-template <int VEC>
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float* x) {
-    if constexpr (VEC == 8) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
-    } else if constexpr (VEC == 4) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack(x[0], x[1]), pack(x[2], x[3]));
-    } else {
-        *p = __float2bfloat16_rn(x[0]);
-    }
+__device__ __forceinline__ void widen(uint32_t u, float (&x)[1], float) { x[0] = __uint_as_float(u); }
+__device__ __forceinline__ void narrow(const float (&x)[8], uint4& u, __nv_bfloat16) {
+    u = make_uint4(narrow(x[0], x[1]), narrow(x[2], x[3]), narrow(x[4], x[5]), narrow(x[6], x[7]));
 }
+__device__ __forceinline__ void narrow(const float (&x)[4], uint2& u, __nv_bfloat16) { u = make_uint2(narrow(x[0], x[1]), narrow(x[2], x[3])); }
+__device__ __forceinline__ void narrow(const float (&x)[1], unsigned short& u, __nv_bfloat16) { u = __bfloat16_as_ushort(__float2bfloat16_rn(x[0])); }
+__device__ __forceinline__ void narrow(const float (&x)[4], uint4& u, float) {
+    u = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+__device__ __forceinline__ void narrow(const float (&x)[1], uint32_t& u, float) { u = __float_as_uint(x[0]); }
 
 // A row's 2 VEC-channel slots: slot s < P / VEC holds VEC pairs, the later ones 2 VEC channels that do not turn.
 // LPR lanes share a row, SPL slots each.
@@ -99,37 +83,43 @@ __device__ __forceinline__ void places(int slot, int P, int* a, int* b) {
         *b = P + VEC * slot;
     }
 }
-// One slot's pairs, pair i in (x[i], x[VEC + i]) (interleaved memory order is a0 b0 a1 b1 ...).
+// One slot as it lies in memory; its pairs, pair i in (x[i], x[VEC + i]) (interleaved memory order is a0 b0 a1 b1 ...).
+template <typename T, int VEC>
+struct Slot {
+    piece_t<T, VEC> a, b;
+};
 template <typename T, int VEC, bool IL>
-__device__ __forceinline__ void load_slot(const T* row, int slot, int P, float* x) {
+__device__ __forceinline__ Slot<T, VEC> load_slot(const T* row, int slot, int P) {
     int a, b;
     places<VEC, IL>(slot, P, &a, &b);
-    float y[2 * VEC];
-    get<VEC>(row + a, y);
-    get<VEC>(row + b, y + VEC);
+    Slot<T, VEC> s;
+    s.a = *reinterpret_cast<const piece_t<T, VEC>*>(row + a);
+    s.b = *reinterpret_cast<const piece_t<T, VEC>*>(row + b);
+    return s;
+}
+template <typename T, int VEC, bool IL>
+__device__ __forceinline__ void pairs_of(const Slot<T, VEC>& s, float (&x)[2 * VEC]) {
+    float y[2][VEC];
+    widen(s.a, y[0], T());
+    widen(s.b, y[1], T());
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-        x[i] = IL ? y[2 * i] : y[i];
-        x[VEC + i] = IL ? y[2 * i + 1] : y[VEC + i];
+        x[i] = IL ? (&y[0][0])[2 * i] : y[0][i];
+        x[VEC + i] = IL ? (&y[0][0])[2 * i + 1] : y[1][i];
     }
 }
 template <typename T, int VEC, bool IL>
-__device__ __forceinline__ void store_slot(T* row, int slot, int P, const float* x) {
+__device__ __forceinline__ void store_slot(T* row, int slot, int P, const float (&x)[2 * VEC]) {
     int a, b;
     places<VEC, IL>(slot, P, &a, &b);
-    float y[2 * VEC];
+    float y[2][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        if (IL) {
-            y[2 * i] = x[i];
-            y[2 * i + 1] = x[VEC + i];
-        } else {
-            y[i] = x[i];
-            y[VEC + i] = x[VEC + i];
-        }
-    }
-    put<VEC>(row + a, y);
-    put<VEC>(row + b, y + VEC);
+    for (int i = 0; i < 2 * VEC; ++i) (&y[0][0])[i] = IL ? x[(i & 1) * VEC + (i >> 1)] : x[i];
+    Slot<T, VEC> s;
+    narrow(y[0], s.a, T());
+    narrow(y[1], s.b, T());
+    *reinterpret_cast<piece_t<T, VEC>*>(row + a) = s.a;
+    *reinterpret_cast<piece_t<T, VEC>*>(row + b) = s.b;
 }
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -138,36 +128,50 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// pos * inv_freq in half turns, in [-1, 1). Turns per position as a 64-bit fraction F (whole turns do not count): the
-// product with 1 / 2 pi as a double and its rest, so F is right to its last bit; pos * F then wraps at whole turns by
-// itself, and the angle is off by |pos| 2^-64 turns.
-__device__ __forceinline__ float position_half_turns(long long pos, float inv_freq) {
-    if (!isfinite(inv_freq)) return __int_as_float(0x7fc00000);
+// Turns per position as a 64-bit fraction (whole turns do not count): the product with 1 / 2 pi as a double and its
+// rest, so it is right to its last bit.
+__device__ __forceinline__ unsigned long long turns_of(float inv_freq) {
     const double f = inv_freq;
     double turns = f * 0.15915494309189535;
     const double rest = fma(f, 0.15915494309189535, -turns) + f * -9.839338337591243e-18;
     turns -= floor(turns);
-    const unsigned long long F = __double2ull_rz(turns * 18446744073709551616.0) +
-                                 (unsigned long long)__double2ll_rn(rest * 18446744073709551616.0);
-    return (float)((double)(long long)((unsigned long long)pos * F) * 0x1p-63);
+    return __double2ull_rz(turns * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(rest * 18446744073709551616.0);
 }
-
-// cos and sin of token t's angles for this lane's slots; `cs` is the warp's own. A pair whose axis does not exist stays.
+// What a block keeps of its pairs: the fraction and the axis (-1: none, the pair stays; -2: not a number).
+struct Pairs {
+    unsigned long long turns[64];
+    int axis[64];
+};
+__device__ __forceinline__ void make_pairs(const QkRopeArgs& a, Pairs& q) {
+    for (int p = threadIdx.x; p < a.pairs; p += 32 * WARPS) {
+        const float f = a.inv_freq[p];
+        int ax = a.axes ? a.axes[p] : 0;
+        if (ax < 0 || ax >= a.num_axes) {
+            ax = -1;
+            atomicOr(&g_rope_error, 1u);
+        } else if (!isfinite(f)) {
+            ax = -2;
+        }
+        q.axis[p] = ax;
+        q.turns[p] = ax >= 0 ? turns_of(f) : 0;
+    }
+    __syncthreads();
+}
+// cos and sin of token t's angles for this lane's slots; `cs` is the warp's own. pos * turns wraps at whole turns by
+// itself, so the angle is off by |pos| 2^-64 turns before it rounds to 32 bits.
 template <int D, int VEC>
-__device__ __forceinline__ void make_angles(const QkRopeArgs& a, long long t, float2* cs,
+__device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q, long long t, float2* cs,
                                             float2 (&mine)[RowLayout<D, VEC>::SPL][VEC]) {
     using L = RowLayout<D, VEC>;
     const int lane = threadIdx.x & 31;
     __syncwarp();
     for (int p = lane; p < a.pairs; p += 32) {
-        const int ax = a.axes ? a.axes[p] : 0;
-        float half_turns = 0.f;
-        if (ax >= 0 && ax < a.num_axes) {
+        const int ax = q.axis[p];
+        float half_turns = ax == -2 ? __int_as_float(0x7fc00000) : 0.f;
+        if (ax >= 0) {
             const long long at = (long long)ax * a.tokens + t;
             const long long pos = a.pos64 ? static_cast<const long long*>(a.positions)[at] : static_cast<const int*>(a.positions)[at];
-            half_turns = position_half_turns(pos, a.inv_freq[p]);
-        } else {
-            atomicOr(&g_rope_error, 1u);
+            half_turns = (float)((int)(((unsigned long long)pos * q.turns[p]) >> 32)) * 0x1p-31f;
         }
         float s, c;
         sincospif(half_turns, &s, &c);
@@ -177,21 +181,24 @@ __device__ __forceinline__ void make_angles(const QkRopeArgs& a, long long t, fl
 #pragma unroll
     for (int j = 0; j < L::SPL; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
+        for (int i = 0; i < VEC; ++i) {   // slots that do not turn: cosine 1, sine 0
             const int p = (lane % L::LPR + j * L::LPR) * VEC + i;
             mine[j][i] = p < a.pairs ? cs[p] : make_float2(1.f, 0.f);
         }
 }
 
-template <typename T, int D, int VEC, bool IL>
-__device__ __forceinline__ void load_weight(const T* w, int sl, int P, float (&g)[RowLayout<D, VEC>::SPL][2 * VEC]) {
+template <int D, int VEC, bool IL>
+__device__ __forceinline__ void load_weight(const float* w, int sl, int P, float (&g)[RowLayout<D, VEC>::SPL][2 * VEC]) {
     using L = RowLayout<D, VEC>;
 #pragma unroll
     for (int j = 0; j < L::SPL; ++j) {
-        if (w) load_slot<float, VEC, IL>(w, sl + j * L::LPR, P, g[j]);
+        int pa, pb;
+        places<VEC, IL>(sl + j * L::LPR, P, &pa, &pb);
 #pragma unroll
-        for (int i = 0; i < 2 * VEC; ++i)
-            if (!w) g[j][i] = 1.f;
+        for (int i = 0; i < 2 * VEC; ++i) {
+            const int at = i < VEC ? (IL ? pa + 2 * i : pa + i) : (IL ? pa + 2 * (i - VEC) + 1 : pb + i - VEC);
+            g[j][i] = w ? w[at] : 1.f;
+        }
     }
 }
 
@@ -200,200 +207,224 @@ template <typename T, int D, int VEC, bool IL, int U>
 __device__ __forceinline__ void rows_fwd(const QkRopeArgs& a, const T* src, T* dst, const float* w, int lo, int hi,
                                          const float2 (&cs)[RowLayout<D, VEC>::SPL][VEC]) {
     using L = RowLayout<D, VEC>;
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR;
+    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR;
     float g[L::SPL][2 * VEC];
-    if (a.norm) load_weight<float, D, VEC, IL>(w, sl, a.pairs, g);
-    for (int r0 = lo + lane / L::LPR; r0 - lane / L::LPR < hi; r0 += U * L::RPW) {
-        float x[U][L::SPL][2 * VEC];
+    if (a.norm) load_weight<D, VEC, IL>(w, sl, a.pairs, g);
+    for (int base = lo; base < hi; base += U * L::RPW) {
+        Slot<T, VEC> raw[U][L::SPL];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < L::SPL; ++j) {
-                if (r0 + u * L::RPW < hi) load_slot<T, VEC, IL>(src + (size_t)(r0 + u * L::RPW) * D, sl + j * L::LPR, a.pairs, x[u][j]);
-                else
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[u][j][i] = 0.f;
+            for (int j = 0; j < L::SPL; ++j) {   // past the last row: that row once more, for the sums; it is not stored
+                const int r = min(base + u * L::RPW + sub, hi - 1);
+                raw[u][j] = load_slot<T, VEC, IL>(src + (size_t)r * D, sl + j * L::LPR, a.pairs);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const int r = base + u * L::RPW + sub;
+            float x[L::SPL][2 * VEC];
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < L::SPL; ++j) {
+                pairs_of<T, VEC, IL>(raw[u][j], x[j]);
+#pragma unroll
+                for (int i = 0; i < 2 * VEC; ++i) sum = fmaf(x[j][i], x[j][i], sum);
+            }
             if (a.norm) {
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < L::SPL; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) sum = fmaf(x[u][j][i], x[u][j][i], sum);
                 const float scale = rsqrtf(row_sum<L::LPR>(sum) * (1.f / D) + a.eps);
 #pragma unroll
                 for (int j = 0; j < L::SPL; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[u][j][i] *= scale * g[j][i];
+                    for (int i = 0; i < 2 * VEC; ++i) x[j][i] *= scale * g[j][i];
             }
-            if (r0 + u * L::RPW < hi)
 #pragma unroll
-                for (int j = 0; j < L::SPL; ++j) {
-                    float y[2 * VEC];
+            for (int j = 0; j < L::SPL; ++j) {
+                if (sl + j * L::LPR < a.pairs / VEC)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {   // slots that do not turn have cosine 1 and sine 0
-                        const float2 c = cs[j][i];
-                        y[i] = x[u][j][i] * c.x - x[u][j][VEC + i] * c.y;
-                        y[VEC + i] = x[u][j][i] * c.y + x[u][j][VEC + i] * c.x;
+                    for (int i = 0; i < VEC; ++i) {
+                        const float xa = x[j][i], xb = x[j][VEC + i];
+                        x[j][i] = xa * cs[j][i].x - xb * cs[j][i].y;
+                        x[j][VEC + i] = xa * cs[j][i].y + xb * cs[j][i].x;
                     }
-                    const bool turns = sl + j * L::LPR < a.pairs / VEC;
-                    store_slot<T, VEC, IL>(dst + (size_t)(r0 + u * L::RPW) * D, sl + j * L::LPR, a.pairs, turns ? y : x[u][j]);
-                }
+                if (r < hi) store_slot<T, VEC, IL>(dst + (size_t)r * D, sl + j * L::LPR, a.pairs, x[j]);
+            }
         }
     }
 }
 
+// Rows of both places that a lane has in flight: 64 bytes of bf16 in 16-byte pieces, as much else.
+template <typename T, int D, int VEC>
+constexpr int rows_in_flight() { return VEC == 1 ? 1 : 64 / (2 * VEC * (int)sizeof(T)); }
+
 template <typename T, int D, int VEC, bool IL>
-__global__ void __launch_bounds__(32 * WARPS) qk_rope_fwd_kernel(const __grid_constant__ QkRopeArgs a) {
+__global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 3) qk_rope_fwd_kernel(const __grid_constant__ QkRopeArgs a) {
     using L = RowLayout<D, VEC>;
-    constexpr int U = VEC == 8 ? 2 : 4;
+    constexpr int U = rows_in_flight<T, D, VEC>();
+    __shared__ Pairs pairs;
     __shared__ float2 cs[WARPS][D / 2];
-    const long long t = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
-    if (t >= a.tokens) return;
-    float2 mine[L::SPL][VEC];
-    make_angles<D, VEC>(a, t, cs[threadIdx.x >> 5], mine);
+    make_pairs(a, pairs);
     const int heads = a.Hq + a.Hk, part = (heads + gridDim.y - 1) / gridDim.y;
     const int lo = blockIdx.y * part, hi = min(heads, lo + part);
-    if (lo < a.Hq)
-        rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.q) + t * a.q_stride, static_cast<T*>(a.q_out) + t * a.Hq * D, a.q_weight,
-                                   lo, min(hi, a.Hq), mine);
-    if (hi > a.Hq)
-        rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.k) + t * a.k_stride, static_cast<T*>(a.k_out) + t * a.Hk * D, a.k_weight,
-                                   max(0, lo - a.Hq), hi - a.Hq, mine);
-}
-
-template <typename T, int D, int VEC, bool IL>
-__device__ __forceinline__ void rows_bwd(const QkRopeArgs& a, const T* src, const T* dy, T* dst, const float* w, int n,
-                                         const float2 (&cs)[RowLayout<D, VEC>::SPL][VEC], float (&dw)[RowLayout<D, VEC>::SPL][2 * VEC]) {
-    using L = RowLayout<D, VEC>;
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR;
-    float g[L::SPL][2 * VEC];
-    if (a.norm) load_weight<float, D, VEC, IL>(w, sl, a.pairs, g);
-    for (int r = lane / L::LPR; r - lane / L::LPR < n; r += L::RPW) {
-        const bool on = r < n;
-        float x[L::SPL][2 * VEC], d[L::SPL][2 * VEC];
-#pragma unroll
-        for (int j = 0; j < L::SPL; ++j) {
-            const int slot = sl + j * L::LPR;
-            if (on) {
-                load_slot<T, VEC, IL>(dy + (size_t)r * D, slot, a.pairs, d[j]);
-                if (a.norm) load_slot<T, VEC, IL>(src + (size_t)r * D, slot, a.pairs, x[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2 * VEC; ++i) {
-                if (!on) d[j][i] = 0.f;
-                if (!on || !a.norm) x[j][i] = 0.f;
-            }
-            if (slot < a.pairs / VEC)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float2 c = cs[j][i];
-                    const float da = d[j][i], db = d[j][VEC + i];
-                    d[j][i] = da * c.x + db * c.y;
-                    d[j][VEC + i] = db * c.x - da * c.y;
-                }
-        }
-        if (a.norm) {
-            float sum = 0.f, dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < L::SPL; ++j)
-#pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) {
-                    sum = fmaf(x[j][i], x[j][i], sum);
-                    dot = fmaf(d[j][i] * g[j][i], x[j][i], dot);
-                }
-            const float rs = rsqrtf(row_sum<L::LPR>(sum) * (1.f / D) + a.eps);
-            const float mean = row_sum<L::LPR>(dot) * rs * (1.f / D);   // mean(d w m)
-#pragma unroll
-            for (int j = 0; j < L::SPL; ++j)
-#pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) {
-                    const float m = x[j][i] * rs;
-                    if (on) dw[j][i] = fmaf(d[j][i], m, dw[j][i]);
-                    d[j][i] = (d[j][i] * g[j][i] - m * mean) * rs;
-                }
-        }
-        if (on)
-#pragma unroll
-            for (int j = 0; j < L::SPL; ++j) store_slot<T, VEC, IL>(dst + (size_t)r * D, sl + j * L::LPR, a.pairs, d[j]);
+    for (long long t = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5); t < a.tokens; t += (long long)gridDim.x * WARPS) {
+        float2 mine[L::SPL][VEC];
+        make_angles<D, VEC>(a, pairs, t, cs[threadIdx.x >> 5], mine);
+        if (lo < a.Hq)
+            rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.q) + t * a.q_stride, static_cast<T*>(a.q_out) + t * a.Hq * D, a.q_weight,
+                                       lo, min(hi, a.Hq), mine);
+        if (hi > a.Hq)
+            rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.k) + t * a.k_stride, static_cast<T*>(a.k_out) + t * a.Hk * D, a.k_weight,
+                                       max(0, lo - a.Hq), hi - a.Hq, mine);
     }
 }
 
+// A block works on one of the two tensors: the first q_blocks on q, the others on k, and keeps one weight's gradient.
 template <typename T, int D, int VEC, bool IL>
-__global__ void __launch_bounds__(32 * WARPS) qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a, float* __restrict__ partial) {
+__global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 2)
+qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a, int q_blocks, float* __restrict__ partial) {
     using L = RowLayout<D, VEC>;
+    constexpr int U = VEC == 1 ? 1 : rows_in_flight<T, D, VEC>() / 2;
+    __shared__ Pairs pairs;
     __shared__ float2 cs[WARPS][D / 2];
-    __shared__ float part[2][WARPS][D];
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR, warp = threadIdx.x >> 5;
-    float dw[2][L::SPL][2 * VEC] = {};
-    for (long long t = (long long)blockIdx.x * WARPS + warp; t < a.tokens; t += (long long)gridDim.x * WARPS) {
-        float2 mine[L::SPL][VEC];
-        make_angles<D, VEC>(a, t, cs[warp], mine);
-        rows_bwd<T, D, VEC, IL>(a, static_cast<const T*>(a.q) + t * a.q_stride, static_cast<const T*>(a.dq_out) + t * a.Hq * D,
-                                static_cast<T*>(a.dq) + t * a.Hq * D, a.q_weight, a.Hq, mine, dw[0]);
-        rows_bwd<T, D, VEC, IL>(a, static_cast<const T*>(a.k) + t * a.k_stride, static_cast<const T*>(a.dk_out) + t * a.Hk * D,
-                                static_cast<T*>(a.dk) + t * a.Hk * D, a.k_weight, a.Hk, mine, dw[1]);
+    __shared__ float part[WARPS][D];
+    make_pairs(a, pairs);
+    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = threadIdx.x >> 5;
+    const bool isq = (int)blockIdx.x < q_blocks;
+    const int block = isq ? blockIdx.x : blockIdx.x - q_blocks, blocks = isq ? q_blocks : gridDim.x - q_blocks;
+    const int n = isq ? a.Hq : a.Hk;
+    float g[L::SPL][2 * VEC], dw[L::SPL][2 * VEC] = {};
+    if (a.norm) load_weight<D, VEC, IL>(isq ? a.q_weight : a.k_weight, sl, a.pairs, g);
+    for (long long t = (long long)block * WARPS + warp; t < a.tokens; t += (long long)blocks * WARPS) {
+        const T* src = isq ? static_cast<const T*>(a.q) + t * a.q_stride : static_cast<const T*>(a.k) + t * a.k_stride;
+        const T* dy = static_cast<const T*>(isq ? a.dq_out : a.dk_out) + t * n * D;
+        T* dst = static_cast<T*>(isq ? a.dq : a.dk) + t * n * D;
+        float2 c[L::SPL][VEC];
+        make_angles<D, VEC>(a, pairs, t, cs[warp], c);
+        for (int base = 0; base < n; base += U * L::RPW) {
+            Slot<T, VEC> rx[U][L::SPL], rd[U][L::SPL];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < L::SPL; ++j) {
+                    const int r = min(base + u * L::RPW + sub, n - 1);
+                    rd[u][j] = load_slot<T, VEC, IL>(dy + (size_t)r * D, sl + j * L::LPR, a.pairs);
+                    if (a.norm) rx[u][j] = load_slot<T, VEC, IL>(src + (size_t)r * D, sl + j * L::LPR, a.pairs);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = base + u * L::RPW + sub;
+                const bool on = r < n;
+                float d[L::SPL][2 * VEC];
+#pragma unroll
+                for (int j = 0; j < L::SPL; ++j) {
+                    pairs_of<T, VEC, IL>(rd[u][j], d[j]);
+                    if (sl + j * L::LPR < a.pairs / VEC)
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            const float da = d[j][i], db = d[j][VEC + i];
+                            d[j][i] = da * c[j][i].x + db * c[j][i].y;
+                            d[j][VEC + i] = db * c[j][i].x - da * c[j][i].y;
+                        }
+                }
+                if (a.norm) {
+                    float x[L::SPL][2 * VEC];
+                    float sum = 0.f, dot = 0.f;
+#pragma unroll
+                    for (int j = 0; j < L::SPL; ++j) {
+                        pairs_of<T, VEC, IL>(rx[u][j], x[j]);
+#pragma unroll
+                        for (int i = 0; i < 2 * VEC; ++i) {
+                            sum = fmaf(x[j][i], x[j][i], sum);
+                            dot = fmaf(d[j][i] * g[j][i], x[j][i], dot);
+                        }
+                    }
+                    const float rs = rsqrtf(row_sum<L::LPR>(sum) * (1.f / D) + a.eps);
+                    const float mean = row_sum<L::LPR>(dot) * rs * (1.f / D);   // mean(d w m)
+#pragma unroll
+                    for (int j = 0; j < L::SPL; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2 * VEC; ++i) {
+                            const float m = x[j][i] * rs;
+                            if (on) dw[j][i] = fmaf(d[j][i], m, dw[j][i]);
+                            d[j][i] = (d[j][i] * g[j][i] - m * mean) * rs;
+                        }
+                }
+                if (on)
+#pragma unroll
+                    for (int j = 0; j < L::SPL; ++j) store_slot<T, VEC, IL>(dst + (size_t)r * D, sl + j * L::LPR, a.pairs, d[j]);
+            }
+        }
     }
     if (!partial) return;
-    // the block's share of the weight gradients: the rows of a warp, then the warps in order
+    // the block's share of the weight's gradient: the rows of a warp, then the warps in order
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
+    for (int j = 0; j < L::SPL; ++j) {
 #pragma unroll
-        for (int j = 0; j < L::SPL; ++j) {
+        for (int i = 0; i < 2 * VEC; ++i)
+#pragma unroll
+            for (int m = L::LPR; m < 32; m <<= 1) dw[j][i] += __shfl_xor_sync(0xffffffffu, dw[j][i], m);
+        int pa, pb;
+        places<VEC, IL>(sl + j * L::LPR, a.pairs, &pa, &pb);
+        if (lane < L::LPR)
 #pragma unroll
             for (int i = 0; i < 2 * VEC; ++i)
-#pragma unroll
-                for (int m = L::LPR; m < 32; m <<= 1) dw[which][j][i] += __shfl_xor_sync(0xffffffffu, dw[which][j][i], m);
-            if (lane < L::LPR) store_slot<float, VEC, IL>(part[which][warp], sl + j * L::LPR, a.pairs, dw[which][j]);
-        }
+                part[warp][i < VEC ? (IL ? pa + 2 * i : pa + i) : (IL ? pa + 2 * (i - VEC) + 1 : pb + i - VEC)] = dw[j][i];
+    }
     __syncthreads();
-    for (int x = threadIdx.x; x < 2 * D; x += 32 * WARPS) {
+    for (int x = threadIdx.x; x < D; x += 32 * WARPS) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < WARPS; ++i) s += part[x / D][i][x % D];
-        partial[(size_t)blockIdx.x * 2 * D + x] = s;
+        for (int i = 0; i < WARPS; ++i) s += part[i][x];
+        partial[(size_t)blockIdx.x * D + x] = s;
     }
 }
 
-// The weight gradients: one block per channel and tensor sums the blocks' shares in a fixed order.
-__global__ void __launch_bounds__(128) qk_rope_weights_kernel(const float* __restrict__ partial, int blocks, int D,
-                                                              float* __restrict__ dwq, float* __restrict__ dwk) {
-    __shared__ float warps[4];
+// The weights' gradients: a block sums 32 channels of one of them over the blocks' shares, 32 runs of them in order.
+__global__ void __launch_bounds__(1024) qk_rope_weights_kernel(const float* __restrict__ partial, int q_blocks, int blocks, int D,
+                                                               float* __restrict__ dwq, float* __restrict__ dwk) {
+    __shared__ float runs[32][33];
+    float* out = blockIdx.y == 0 ? dwq : dwk;
+    if (!out) return;
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, ch = blockIdx.x * 32 + c;
+    const int from = blockIdx.y == 0 ? 0 : q_blocks, to = blockIdx.y == 0 ? q_blocks : blocks;
     float s = 0.f;
-    for (int i = threadIdx.x; i < blocks; i += 128) s += partial[(size_t)i * 2 * D + blockIdx.x];
-    s = row_sum<32>(s);
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = s;
+    if (ch < D)
+#pragma unroll 4
+        for (int i = from + g; i < to; i += 32) s += partial[(size_t)i * D + ch];
+    runs[c][g] = s;
     __syncthreads();
-    if (threadIdx.x) return;
-    s = (warps[0] + warps[1]) + (warps[2] + warps[3]);
-    float* out = (int)blockIdx.x < D ? dwq : dwk;
-    if (out) out[blockIdx.x % D] = s;
+    s = row_sum<32>(runs[g][c]);
+    if (c == 0 && blockIdx.x * 32 + g < D) out[blockIdx.x * 32 + g] = s;
 }
 
 template <typename T, int D, int VEC, bool IL>
 cudaError_t run(const QkRopeArgs& a, float* ws, cudaStream_t s) {
     const long long blocks = (a.tokens + WARPS - 1) / WARPS;
     if (!a.dq) {
-        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share
+        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share; many:
+        // three blocks an SM take them in turn
         const int rows = (a.Hq + a.Hk + RowLayout<D, VEC>::RPW - 1) / RowLayout<D, VEC>::RPW;
-        const long long want = (148 * 2 + blocks - 1) / blocks;
+        const long long want = (148 + blocks - 1) / blocks;
         const int parts = (int)(want < rows ? want : rows);
+        const int grid = (int)(blocks < 148 * 3 ? blocks : 148 * 3);
         TraceScope trace(K_QK_ROPE, s);
-        qk_rope_fwd_kernel<T, D, VEC, IL><<<dim3((unsigned)blocks, parts), 32 * WARPS, 0, s>>>(a);
+        qk_rope_fwd_kernel<T, D, VEC, IL><<<dim3(grid, parts), 32 * WARPS, 0, s>>>(a);
         return cudaGetLastError();
     }
-    const int grid = (int)(blocks < QK_ROPE_BLOCKS ? blocks : QK_ROPE_BLOCKS);
+    // two blocks an SM, shared out by the tensors' rows
+    int q_blocks = (int)((long long)QK_ROPE_BLOCKS * a.Hq / (a.Hq + a.Hk));
+    int k_blocks = QK_ROPE_BLOCKS - (q_blocks = q_blocks < 1 ? 1 : q_blocks);
+    if (k_blocks < 1) k_blocks = 1, q_blocks = QK_ROPE_BLOCKS - 1;
+    q_blocks = (int)(blocks < q_blocks ? blocks : q_blocks);
+    k_blocks = (int)(blocks < k_blocks ? blocks : k_blocks);
     const bool weights = a.norm && (a.dq_weight || a.dk_weight);
     {
         TraceScope trace(K_QK_ROPE_BWD, s);
-        qk_rope_bwd_kernel<T, D, VEC, IL><<<grid, 32 * WARPS, 0, s>>>(a, weights ? ws : nullptr);
+        qk_rope_bwd_kernel<T, D, VEC, IL><<<q_blocks + k_blocks, 32 * WARPS, 0, s>>>(a, q_blocks, weights ? ws : nullptr);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !weights) return e;
     TraceScope trace(K_QK_ROPE_BWD, s);
-    qk_rope_weights_kernel<<<2 * D, 128, 0, s>>>(ws, grid, D, a.dq_weight, a.dk_weight);
+    qk_rope_weights_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, s>>>(ws, q_blocks, q_blocks + k_blocks, D, a.dq_weight, a.dk_weight);
     return cudaGetLastError();
 }
 template <typename T, int D>

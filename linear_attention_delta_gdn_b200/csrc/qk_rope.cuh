@@ -25,7 +25,7 @@ struct QkRopeArgs {
     void *dq, *dk;
     float *dq_weight, *dk_weight;     // or null
 };
-constexpr int QK_ROPE_BLOCKS = 148 * 8;   // blocks of the backward at most: each leaves one partial sum of the weight gradients
+constexpr int QK_ROPE_BLOCKS = 148 * 2;   // blocks of the backward at most: each leaves one weight's partial gradient
 cudaError_t qk_rope_launch(const QkRopeArgs& a, float* ws, cudaStream_t s);
 cudaError_t qk_rope_take_errors(unsigned int* bits);
 
