@@ -175,7 +175,7 @@ __device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q,
         }
         float s, c;
         sincospif(half_turns, &s, &c);
-        cs[p] = make_float2(c, s);
+        cs[p + 2 * (p / VEC)] = make_float2(c, s);   // 16 bytes of shift a lane's pairs: no bank twice
     }
     __syncwarp();
 #pragma unroll
@@ -183,7 +183,7 @@ __device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q,
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {   // slots that do not turn: cosine 1, sine 0
             const int p = (lane % L::LPR + j * L::LPR) * VEC + i;
-            mine[j][i] = p < a.pairs ? cs[p] : make_float2(1.f, 0.f);
+            mine[j][i] = p < a.pairs ? cs[p + 2 * (p / VEC)] : make_float2(1.f, 0.f);
         }
 }
 
@@ -202,89 +202,83 @@ __device__ __forceinline__ void load_weight(const float* w, int sl, int P, float
     }
 }
 
-// Rows lo .. hi - 1 of one token and tensor: U rows a lane in flight.
-template <typename T, int D, int VEC, bool IL, int U>
-__device__ __forceinline__ void rows_fwd(const QkRopeArgs& a, const T* src, T* dst, const float* w, int lo, int hi,
-                                         const float2 (&cs)[RowLayout<D, VEC>::SPL][VEC]) {
+// Rows of both places that a lane has in flight: 64 bytes of bf16 in 16-byte pieces, as much else.
+template <typename T, int D, int VEC>
+constexpr int rows_in_flight() { return VEC == 1 ? 1 : 64 / (2 * VEC * (int)sizeof(T)); }
+
+// A block works on one of the two tensors, the first q_blocks on q, the others on k, and keeps its weight in registers;
+// blockIdx.y takes a part of the heads.
+template <typename T, int D, int VEC, bool IL>
+__global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 3) qk_rope_fwd_kernel(const __grid_constant__ QkRopeArgs a, int q_blocks) {
     using L = RowLayout<D, VEC>;
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR;
+    constexpr int U = rows_in_flight<T, D, VEC>();
+    __shared__ Pairs pairs;
+    __shared__ __align__(16) float2 cs[WARPS][D / 2 + 2 * (D / 2 / VEC)];
+    make_pairs(a, pairs);
+    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = threadIdx.x >> 5;
+    const bool isq = (int)blockIdx.x < q_blocks;
+    const int block = isq ? blockIdx.x : blockIdx.x - q_blocks, blocks = isq ? q_blocks : gridDim.x - q_blocks;
+    const int n = isq ? a.Hq : a.Hk, part = (n + gridDim.y - 1) / gridDim.y;
+    const int lo = blockIdx.y * part, hi = min(n, lo + part);
+    if (lo >= hi) return;
     float g[L::SPL][2 * VEC];
-    if (a.norm) load_weight<D, VEC, IL>(w, sl, a.pairs, g);
-    for (int base = lo; base < hi; base += U * L::RPW) {
-        Slot<T, VEC> raw[U][L::SPL];
+    if (a.norm) load_weight<D, VEC, IL>(isq ? a.q_weight : a.k_weight, sl, a.pairs, g);
+    for (long long t = (long long)block * WARPS + warp; t < a.tokens; t += (long long)blocks * WARPS) {
+        const T* src = isq ? static_cast<const T*>(a.q) + t * a.q_stride : static_cast<const T*>(a.k) + t * a.k_stride;
+        T* dst = static_cast<T*>(isq ? a.q_out : a.k_out) + t * n * D;
+        float2 c[L::SPL][VEC];
+        make_angles<D, VEC>(a, pairs, t, cs[warp], c);
+        for (int base = lo; base < hi; base += U * L::RPW) {
+            Slot<T, VEC> raw[U][L::SPL];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < L::SPL; ++j) {   // past the last row: that row once more, for the sums; it is not stored
-                const int r = min(base + u * L::RPW + sub, hi - 1);
-                raw[u][j] = load_slot<T, VEC, IL>(src + (size_t)r * D, sl + j * L::LPR, a.pairs);
-            }
+                for (int j = 0; j < L::SPL; ++j) {   // past the last row: that row once more, for the sums; it is not stored
+                    const int r = min(base + u * L::RPW + sub, hi - 1);
+                    raw[u][j] = load_slot<T, VEC, IL>(src + (size_t)r * D, sl + j * L::LPR, a.pairs);
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = base + u * L::RPW + sub;
-            float x[L::SPL][2 * VEC];
-            float sum = 0.f;
+            for (int u = 0; u < U; ++u) {
+                const int r = base + u * L::RPW + sub;
+                float x[L::SPL][2 * VEC];
+                float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < L::SPL; ++j) {
-                pairs_of<T, VEC, IL>(raw[u][j], x[j]);
+                for (int j = 0; j < L::SPL; ++j) {
+                    pairs_of<T, VEC, IL>(raw[u][j], x[j]);
 #pragma unroll
-                for (int i = 0; i < 2 * VEC; ++i) sum = fmaf(x[j][i], x[j][i], sum);
-            }
-            if (a.norm) {
-                const float scale = rsqrtf(row_sum<L::LPR>(sum) * (1.f / D) + a.eps);
+                    for (int i = 0; i < 2 * VEC; ++i) sum = fmaf(x[j][i], x[j][i], sum);
+                }
+                if (a.norm) {
+                    const float scale = rsqrtf(row_sum<L::LPR>(sum) * (1.f / D) + a.eps);
 #pragma unroll
-                for (int j = 0; j < L::SPL; ++j)
+                    for (int j = 0; j < L::SPL; ++j)
 #pragma unroll
-                    for (int i = 0; i < 2 * VEC; ++i) x[j][i] *= scale * g[j][i];
-            }
+                        for (int i = 0; i < 2 * VEC; ++i) x[j][i] *= scale * g[j][i];
+                }
 #pragma unroll
-            for (int j = 0; j < L::SPL; ++j) {
-                if (sl + j * L::LPR < a.pairs / VEC)
+                for (int j = 0; j < L::SPL; ++j) {
+                    if (sl + j * L::LPR < a.pairs / VEC)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float xa = x[j][i], xb = x[j][VEC + i];
-                        x[j][i] = xa * cs[j][i].x - xb * cs[j][i].y;
-                        x[j][VEC + i] = xa * cs[j][i].y + xb * cs[j][i].x;
-                    }
-                if (r < hi) store_slot<T, VEC, IL>(dst + (size_t)r * D, sl + j * L::LPR, a.pairs, x[j]);
+                        for (int i = 0; i < VEC; ++i) {
+                            const float xa = x[j][i], xb = x[j][VEC + i];
+                            x[j][i] = xa * c[j][i].x - xb * c[j][i].y;
+                            x[j][VEC + i] = xa * c[j][i].y + xb * c[j][i].x;
+                        }
+                    if (r < hi) store_slot<T, VEC, IL>(dst + (size_t)r * D, sl + j * L::LPR, a.pairs, x[j]);
+                }
             }
         }
     }
 }
 
-// Rows of both places that a lane has in flight: 64 bytes of bf16 in 16-byte pieces, as much else.
-template <typename T, int D, int VEC>
-constexpr int rows_in_flight() { return VEC == 1 ? 1 : 64 / (2 * VEC * (int)sizeof(T)); }
-
-template <typename T, int D, int VEC, bool IL>
-__global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 3) qk_rope_fwd_kernel(const __grid_constant__ QkRopeArgs a) {
-    using L = RowLayout<D, VEC>;
-    constexpr int U = rows_in_flight<T, D, VEC>();
-    __shared__ Pairs pairs;
-    __shared__ float2 cs[WARPS][D / 2];
-    make_pairs(a, pairs);
-    const int heads = a.Hq + a.Hk, part = (heads + gridDim.y - 1) / gridDim.y;
-    const int lo = blockIdx.y * part, hi = min(heads, lo + part);
-    for (long long t = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5); t < a.tokens; t += (long long)gridDim.x * WARPS) {
-        float2 mine[L::SPL][VEC];
-        make_angles<D, VEC>(a, pairs, t, cs[threadIdx.x >> 5], mine);
-        if (lo < a.Hq)
-            rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.q) + t * a.q_stride, static_cast<T*>(a.q_out) + t * a.Hq * D, a.q_weight,
-                                       lo, min(hi, a.Hq), mine);
-        if (hi > a.Hq)
-            rows_fwd<T, D, VEC, IL, U>(a, static_cast<const T*>(a.k) + t * a.k_stride, static_cast<T*>(a.k_out) + t * a.Hk * D, a.k_weight,
-                                       max(0, lo - a.Hq), hi - a.Hq, mine);
-    }
-}
-
-// A block works on one of the two tensors: the first q_blocks on q, the others on k, and keeps one weight's gradient.
+// The same split; a block keeps one weight's gradient.
 template <typename T, int D, int VEC, bool IL>
 __global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 2)
 qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a, int q_blocks, float* __restrict__ partial) {
     using L = RowLayout<D, VEC>;
     constexpr int U = VEC == 1 ? 1 : rows_in_flight<T, D, VEC>() / 2;
     __shared__ Pairs pairs;
-    __shared__ float2 cs[WARPS][D / 2];
+    __shared__ __align__(16) float2 cs[WARPS][D / 2 + 2 * (D / 2 / VEC)];
     __shared__ float part[WARPS][D];
     make_pairs(a, pairs);
     const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = threadIdx.x >> 5;
@@ -399,23 +393,22 @@ __global__ void __launch_bounds__(1024) qk_rope_weights_kernel(const float* __re
 template <typename T, int D, int VEC, bool IL>
 cudaError_t run(const QkRopeArgs& a, float* ws, cudaStream_t s) {
     const long long blocks = (a.tokens + WARPS - 1) / WARPS;
-    if (!a.dq) {
-        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share; many:
-        // three blocks an SM take them in turn
-        const int rows = (a.Hq + a.Hk + RowLayout<D, VEC>::RPW - 1) / RowLayout<D, VEC>::RPW;
-        const long long want = (148 + blocks - 1) / blocks;
-        const int parts = (int)(want < rows ? want : rows);
-        const int grid = (int)(blocks < 148 * 3 ? blocks : 148 * 3);
-        TraceScope trace(K_QK_ROPE, s);
-        qk_rope_fwd_kernel<T, D, VEC, IL><<<dim3(grid, parts), 32 * WARPS, 0, s>>>(a);
-        return cudaGetLastError();
-    }
-    // two blocks an SM, shared out by the tensors' rows
-    int q_blocks = (int)((long long)QK_ROPE_BLOCKS * a.Hq / (a.Hq + a.Hk));
-    int k_blocks = QK_ROPE_BLOCKS - (q_blocks = q_blocks < 1 ? 1 : q_blocks);
-    if (k_blocks < 1) k_blocks = 1, q_blocks = QK_ROPE_BLOCKS - 1;
+    // blocks that run at once (three an SM, backwards two), shared out by the tensors' rows
+    const int most = a.dq ? QK_ROPE_BLOCKS : 148 * 3;
+    int q_blocks = (int)((long long)most * a.Hq / (a.Hq + a.Hk));
+    q_blocks = q_blocks < 1 ? 1 : q_blocks > most - 1 ? most - 1 : q_blocks;
+    int k_blocks = most - q_blocks;
     q_blocks = (int)(blocks < q_blocks ? blocks : q_blocks);
     k_blocks = (int)(blocks < k_blocks ? blocks : k_blocks);
+    if (!a.dq) {
+        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share
+        const int rows = ((a.Hq > a.Hk ? a.Hq : a.Hk) + RowLayout<D, VEC>::RPW - 1) / RowLayout<D, VEC>::RPW;
+        const long long want = (148 + 2 * blocks - 1) / (2 * blocks);
+        const int parts = (int)(want < rows ? want : rows);
+        TraceScope trace(K_QK_ROPE, s);
+        qk_rope_fwd_kernel<T, D, VEC, IL><<<dim3(q_blocks + k_blocks, parts), 32 * WARPS, 0, s>>>(a, q_blocks);
+        return cudaGetLastError();
+    }
     const bool weights = a.norm && (a.dq_weight || a.dk_weight);
     {
         TraceScope trace(K_QK_ROPE_BWD, s);
