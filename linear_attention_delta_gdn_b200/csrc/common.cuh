@@ -31,6 +31,23 @@ __host__ __device__ __forceinline__ size_t tok_off(int b, int t, int h, int T, i
 
 __device__ __forceinline__ float fast_exp(float x) { return exp2f(x * 1.4426950408889634f); }
 
+// Two 32-bit operations in one issue slot (sm_100; the rate is that of single ones, the slots are what warps compete for).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
+}
+
 // Index checks of the debug build (compiled with -DGDN2_DEBUG into libgdn2_debug.so). GDN2_IN(word, cond) is
 // true when cond holds; otherwise it sets GDN2_DBG_BIT in the kernel's error word and is false, and the caller
 // skips the access it guards, so the kernel returns normally and gdn2_device_status reports the failure.

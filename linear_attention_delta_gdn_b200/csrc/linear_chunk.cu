@@ -180,23 +180,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
     return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-// Two 32-bit operations in one issue slot (the rate is that of single ones; slots are what the warps compete for).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-          "l"(reinterpret_cast<unsigned long long&>(c)));
-    return r;
-}
-
 // ------------------------------------------------------------ warp 0: loads
 
 template <int DRP, bool STATES>

@@ -137,6 +137,13 @@ __device__ __forceinline__ unsigned long long turns_of(float inv_freq) {
     turns -= floor(turns);
     return __double2ull_rz(turns * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(rest * 18446744073709551616.0);
 }
+// The thread's index, read once (the compiler would read the special register again wherever registers are short, and a
+// read takes as long as a shuffle).
+__device__ __forceinline__ int thread_index() {
+    int t;
+    asm volatile("mov.u32 %0, %tid.x;" : "=r"(t));
+    return t;
+}
 // What a block keeps of its pairs: the fraction and the axis (-1: none, the pair stays; -2: not a number).
 struct Pairs {
     unsigned long long turns[64];
@@ -159,11 +166,10 @@ __device__ __forceinline__ void make_pairs(const QkRopeArgs& a, Pairs& q) {
 }
 // cos and sin of token t's angles for this lane's slots; `cs` is the warp's own. pos * turns wraps at whole turns by
 // itself, so the angle is off by |pos| 2^-64 turns before it rounds to 32 bits.
-template <int D, int VEC>
-__device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q, long long t, float2* cs,
+template <typename T, int D, int VEC>
+__device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q, long long t, int lane, float2* cs,
                                             float2 (&mine)[RowLayout<D, VEC>::SPL][VEC]) {
     using L = RowLayout<D, VEC>;
-    const int lane = threadIdx.x & 31;
     __syncwarp();
     for (int p = lane; p < a.pairs; p += 32) {
         const int ax = q.axis[p];
@@ -174,17 +180,16 @@ __device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q,
             half_turns = (float)((int)(((unsigned long long)pos * q.turns[p]) >> 32)) * 0x1p-31f;
         }
         float s, c;
-        sincospif(half_turns, &s, &c);
-        cs[p + 2 * (p / VEC)] = make_float2(c, s);   // 16 bytes of shift a lane's pairs: no bank twice
+        if (sizeof(T) == 2) __sincosf(half_turns * 3.14159265f, &s, &c);   // off by 2^-21 on [-pi, pi]: the outputs have 8 bits
+        else sincospif(half_turns, &s, &c);
+        cs[p / VEC * (VEC + 2) + p % VEC] = make_float2(c, s);   // 16 bytes of shift a lane's pairs: no bank twice
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < L::SPL; ++j)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {   // slots that do not turn: cosine 1, sine 0
-            const int p = (lane % L::LPR + j * L::LPR) * VEC + i;
-            mine[j][i] = p < a.pairs ? cs[p + 2 * (p / VEC)] : make_float2(1.f, 0.f);
-        }
+        for (int i = 0; i < VEC; ++i)   // of slots that do not turn whatever lies there: they are not used
+            mine[j][i] = cs[(lane % L::LPR + j * L::LPR) * (VEC + 2) + i];
 }
 
 template <int D, int VEC, bool IL>
@@ -202,6 +207,14 @@ __device__ __forceinline__ void load_weight(const float* w, int sl, int P, float
     }
 }
 
+// A token's rows into L2, a 128-byte line a lane: the warp's next token, while it works on this one.
+template <typename T>
+__device__ __forceinline__ void rows_ahead(const T* p, int elements, int lane) {
+    const char* c = reinterpret_cast<const char*>(p);
+    for (int at = lane * 128; at < elements * (int)sizeof(T); at += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(c + at));
+}
+
 // Rows of both places that a lane has in flight: 64 bytes of bf16 in 16-byte pieces, as much else.
 template <typename T, int D, int VEC>
 constexpr int rows_in_flight() { return VEC == 1 ? 1 : 64 / (2 * VEC * (int)sizeof(T)); }
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 3) qk_rope_fwd_kern
     __shared__ Pairs pairs;
     __shared__ __align__(16) float2 cs[WARPS][D / 2 + 2 * (D / 2 / VEC)];
     make_pairs(a, pairs);
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = threadIdx.x >> 5;
+    const int tid = thread_index(), lane = tid & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = tid >> 5;
     const bool isq = (int)blockIdx.x < q_blocks;
     const int block = isq ? blockIdx.x : blockIdx.x - q_blocks, blocks = isq ? q_blocks : gridDim.x - q_blocks;
     const int n = isq ? a.Hq : a.Hk, part = (n + gridDim.y - 1) / gridDim.y;
@@ -226,8 +239,10 @@ __global__ void __launch_bounds__(32 * WARPS, VEC == 1 ? 1 : 3) qk_rope_fwd_kern
     for (long long t = (long long)block * WARPS + warp; t < a.tokens; t += (long long)blocks * WARPS) {
         const T* src = isq ? static_cast<const T*>(a.q) + t * a.q_stride : static_cast<const T*>(a.k) + t * a.k_stride;
         T* dst = static_cast<T*>(isq ? a.q_out : a.k_out) + t * n * D;
+        const long long next = (long long)blocks * WARPS;
+        if (t + next < a.tokens) rows_ahead(src + next * (isq ? a.q_stride : a.k_stride), n * D, lane);
         float2 c[L::SPL][VEC];
-        make_angles<D, VEC>(a, pairs, t, cs[warp], c);
+        make_angles<T, D, VEC>(a, pairs, t, lane, cs[warp], c);
         for (int base = lo; base < hi; base += U * L::RPW) {
             Slot<T, VEC> raw[U][L::SPL];
 #pragma unroll
@@ -281,7 +296,7 @@ qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a, int q_blocks, float* __
     __shared__ __align__(16) float2 cs[WARPS][D / 2 + 2 * (D / 2 / VEC)];
     __shared__ float part[WARPS][D];
     make_pairs(a, pairs);
-    const int lane = threadIdx.x & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = threadIdx.x >> 5;
+    const int tid = thread_index(), lane = tid & 31, sl = lane % L::LPR, sub = lane / L::LPR, warp = tid >> 5;
     const bool isq = (int)blockIdx.x < q_blocks;
     const int block = isq ? blockIdx.x : blockIdx.x - q_blocks, blocks = isq ? q_blocks : gridDim.x - q_blocks;
     const int n = isq ? a.Hq : a.Hk;
@@ -291,8 +306,13 @@ qk_rope_bwd_kernel(const __grid_constant__ QkRopeArgs a, int q_blocks, float* __
         const T* src = isq ? static_cast<const T*>(a.q) + t * a.q_stride : static_cast<const T*>(a.k) + t * a.k_stride;
         const T* dy = static_cast<const T*>(isq ? a.dq_out : a.dk_out) + t * n * D;
         T* dst = static_cast<T*>(isq ? a.dq : a.dk) + t * n * D;
+        const long long next = (long long)blocks * WARPS;
+        if (t + next < a.tokens) {
+            rows_ahead(dy + next * n * D, n * D, lane);
+            if (a.norm) rows_ahead(src + next * (isq ? a.q_stride : a.k_stride), n * D, lane);
+        }
         float2 c[L::SPL][VEC];
-        make_angles<D, VEC>(a, pairs, t, cs[warp], c);
+        make_angles<T, D, VEC>(a, pairs, t, lane, cs[warp], c);
         for (int base = 0; base < n; base += U * L::RPW) {
             Slot<T, VEC> rx[U][L::SPL], rd[U][L::SPL];
 #pragma unroll
@@ -393,9 +413,11 @@ __global__ void __launch_bounds__(1024) qk_rope_weights_kernel(const float* __re
 template <typename T, int D, int VEC, bool IL>
 cudaError_t run(const QkRopeArgs& a, float* ws, cudaStream_t s) {
     const long long blocks = (a.tokens + WARPS - 1) / WARPS;
-    // blocks that run at once (three an SM, backwards two), shared out by the tensors' rows
+    // blocks that run at once (three an SM, backwards two), shared out by the work a token is: a warp's passes over its
+    // heads, and about one and a half more for its angles
     const int most = a.dq ? QK_ROPE_BLOCKS : 148 * 3;
-    int q_blocks = (int)((long long)most * a.Hq / (a.Hq + a.Hk));
+    const auto work = [](int heads) { return 2ll * ((heads + RowLayout<D, VEC>::RPW - 1) / RowLayout<D, VEC>::RPW) + 3; };
+    int q_blocks = (int)(most * work(a.Hq) / (work(a.Hq) + work(a.Hk)));
     q_blocks = q_blocks < 1 ? 1 : q_blocks > most - 1 ? most - 1 : q_blocks;
     int k_blocks = most - q_blocks;
     q_blocks = (int)(blocks < q_blocks ? blocks : q_blocks);
