@@ -50,7 +50,7 @@ struct Pass {
     const void* z_ptr;
     const float* start;      // state in front of the first (behind the last) token, [N, H, Dk, Dv], or null
     float* end;              // the state at the other end, or null
-    float* seg;              // the segments' own states, [N, H, seg, slice][SL][DRP], or null
+    float* seg;              // the segments' own states, [slot, H, slice][SL][DRP], or null
     void* out_ptr;           // the tensor behind out, for a sequence's last, partial chunk
     int start_transposed;    // start is [DZ][DR]
     int rev;
@@ -98,6 +98,13 @@ __device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
     }
     t->l2 = linear::log2_decay(p.log_decay, t->h);
 }
+// Where a segment's own state lies. Sequence n's segments take the slots from row0 / S + n on, S the tokens of a segment:
+// ceil(len / S) of them never reach (row0 + len) / S + n + 1, where the next sequence's begin.
+template <int DRP>
+__device__ __forceinline__ float* segment_state(const Params& p, const Item& t, int seg) {
+    const long long slot = t.row0 / (p.cps * CT) + t.n + seg;
+    return t.p->seg + ((slot * p.seq.H + t.h) * p.slices + t.slice) * (long long)(SL * DRP);
+}
 // The block's first item is found once, before the roles start (its loads and the first reads of the parameters take as
 // long as a chunk).
 __device__ __forceinline__ Item& first_item() {
@@ -117,20 +124,25 @@ struct Cfg {
     static constexpr uint32_t XB = STATES ? 0 : CT * DRP * 2;      // bytes of a row-operand tile
     static constexpr uint32_t YB = CT * DRP * 2;
     static constexpr uint32_t ZB = CT * SL * 2;
-    static constexpr int STAGES = (DRP == 128 && !STATES) ? 2 : 4; // of X and Y
+    static constexpr int STAGES = DRP == 64 ? 4 : STATES ? 3 : 2;  // of X and Y
+    static constexpr int BUF = STATES ? 2 : 1;                     // of Zh, Zl and D: states alone leave room for two
     static constexpr int ZRAW = STATES ? 0 : 2;                    // Z as it is, for P Z
     static constexpr uint32_t SB = STATES ? 0 : DRP * SL * 2;      // bf16 copy of the state
     static constexpr uint32_t OB = STATES ? 0 : CT * SL * 2;       // output staging
     static constexpr uint32_t OFF_Y = STAGES * XB, OFF_Z = OFF_Y + STAGES * YB, OFF_ZH = OFF_Z + ZRAW * ZB,
-                              OFF_ZL = OFF_ZH + ZB, OFF_S = OFF_ZL + ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
+                              OFF_S = OFF_ZH + BUF * 2 * ZB, OFF_O = OFF_S + SB, TOTAL = OFF_O + OB;
     static constexpr uint32_t SMEM = TOTAL + 1024;                 // tiles start on 1024 bytes
     // TMEM columns: A twice (then P in its first half), D (its Zh and its Zl part), O1, O2
     static constexpr uint32_t T_A = 0, T_D = 256, T_O1 = 384, T_O2 = 448;
 };
 
+// What the warps tell one another. A commit behind each product costs the tensor pipe time, so there is one for each: D
+// done gives back its stage's Y and with it Zh and Zl, O1 done its X and the copy of the state, O2 done Z and P.
 struct Bars {
-    uint64_t full[4], empty_x[4], empty_y[4];
-    uint64_t a_full[2], a_free[2], p_full[2], z_full, d_full, d_free, s_full, s_free, o_full, o_free, drain;
+    uint64_t full[4], d_done[4], o1_done[4];                // by stage
+    uint64_t a_full[2], p_full[2], o2_done[2];              // by A's buffer
+    uint64_t z_full[2], d_free[2];                          // by D's buffer
+    uint64_t s_full, o_free, drain;
 };
 
 // The chunk loops of five kinds of warps share one instruction cache, and a loop that runs through it straight costs
@@ -206,14 +218,14 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
             const uint32_t s = ny % K::STAGES, ph = ((ny / K::STAGES) & 1) ^ 1;
             if (i + AHEAD < t.count()) into_l2(t, i + AHEAD);
             const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
-            if (!(ok = wait(&b.empty_y[s], ph))) break;
+            if (!(ok = wait(&b.d_done[s], ph))) break;
             mbar_arrive_expect_tx(&b.full[s], K::YB);
 #pragma unroll
             for (int c = 0; c < DRP / 64; ++c)
                 tma_load_3d(sm + K::OFF_Y + s * K::YB + c * CT * 128, &t.p->y, 64 * c, t.h, row, &b.full[s]);
             ++ny;
             if (!STATES) {   // X and Y come back at different times, and are waited for together
-                if (!(ok = wait(&b.empty_x[s], ph))) break;
+                if (!(ok = wait(&b.o1_done[s], ph))) break;
                 mbar_arrive_expect_tx(&b.full[s], K::XB);
 #pragma unroll
                 for (int c = 0; c < DRP / 64; ++c)
@@ -270,7 +282,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         const uint32_t n = c.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, dph = (n >> 1) & 1;
         const bool ragged = c.ragged_end && c.i == (c.rev ? 0 : c.count - 1);
         // behind a sequence's end the tiles hold another's rows: warpgroup 2 clears them first
-        ok = wait2(&b.full[s], ph, &b.a_free[d], dph ^ 1) && (!ragged || wait(&b.z_full, n & 1));
+        ok = wait2(&b.full[s], ph, &b.o2_done[d], dph ^ 1) && (!ragged || wait(&b.z_full[n % K::BUF], (n / K::BUF) & 1));
         if (!ok) return;
         tc_fence_after();
         const uint64_t xk = x_k + s * (K::XB >> 4), yk = y_k + s * (K::YB >> 4);
@@ -290,13 +302,13 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         ++cur.i;
         ++cur.n;
         if (STATES && !(ok = wait(&b.full[s], ph))) break;   // else A has waited for it
-        if (!(ok = wait2(&b.z_full, one, &b.d_free, one ^ 1))) break;
+        const uint32_t zb = n % K::BUF, zph = (n / K::BUF) & 1;
+        if (!(ok = wait2(&b.z_full[zb], zph, &b.d_free[zb], zph ^ 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)   // Zh and Zl are the two panels of one operand of 128 columns: Y is read once
-            mma_bf16(tm + K::T_D, ymn + MN * kk, zh_mn + MN * kk, idD, kk > 0);
-        mma_commit(&b.d_full);
-        mma_commit(&b.empty_y[s]);
+            mma_bf16(tm + K::T_D + zb * 2 * SL, ymn + MN * kk, zh_mn + zb * (2 * K::ZB >> 4) + MN * kk, idD, kk > 0);
+        mma_commit(&b.d_done[s]);
         if (STATES) continue;
         if (settle(ahead)) issue_pairs(ahead);
         if (!(ok = ok && wait2(&b.s_full, one, &b.o_free, one ^ 1))) break;
@@ -304,15 +316,13 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
 #pragma unroll 1
         for (int kk = 0; kk < DRP / 16; ++kk)
             mma_bf16(tm + K::T_O1, xk + k_step(kk), s_mn + MN * kk, idO, kk > 0);
-        mma_commit(&b.s_free);
-        mma_commit(&b.empty_x[s]);
+        mma_commit(&b.o1_done[s]);
         if (!(ok = wait(&b.p_full[d], (n >> 1) & 1))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int kk = 0; kk < CT / 16; ++kk)
             mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
-        mma_commit(&b.o_full);
-        mma_commit(&b.a_free[d]);
+        mma_commit(&b.o2_done[d]);
     }
     if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
     // what was issued ends before TMEM is given back
@@ -341,7 +351,7 @@ __device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uin
     const float e = q.l2 >= MILD ? linear::decay_pow(q.l2, rev ? 31 - lane : lane) : 1.f;
     const uint32_t quarter = (uint32_t)(32 * w) << 16;
     if (lane == 0) bulk_wait_read();   // the last store has read the staging rows
-    if (!warp_wait(&b.o_full, n & 1)) return false;
+    if (!warp_wait(&b.o2_done[n & 1], (n >> 1) & 1)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
@@ -531,11 +541,12 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
         for (int k = 0; k < 8; ++k) z[k] = ahead[k];
         more = next();
         if (more) load();
-        // Zh and Zl are free once the last chunk's D is done, this copy of Z once the chunk before that has its O2
-        if (n > 0 && !warp_wait(&b.d_full, (n - 1) & 1)) return;
-        if (!STATES && !warp_wait(&b.a_free[n & 1], ((n >> 1) & 1) ^ 1)) return;
+        // Zh and Zl are free once the D that read them is done, this copy of Z once the chunk before that has its O2
+        const uint32_t zb = n % K::BUF, m = n - K::BUF;
+        if (n >= (uint32_t)K::BUF && !warp_wait(&b.d_done[m % K::STAGES], (m / K::STAGES) & 1)) return;
+        if (!STATES && !warp_wait(&b.o2_done[n & 1], ((n >> 1) & 1) ^ 1)) return;
         unsigned char* Z = sm + K::OFF_Z + (n & 1) * K::ZB;
-        unsigned char *Zh = sm + K::OFF_ZH, *Zl = sm + K::OFF_ZL;
+        unsigned char *Zh = sm + K::OFF_ZH + zb * 2 * K::ZB, *Zl = Zh + K::ZB;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             uint4 hi, lo;
@@ -557,7 +568,7 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
                     *reinterpret_cast<uint4*>(sm + K::OFF_Y + s * K::YB + tile_chunk_off(CT, tid, q)) = make_uint4(0, 0, 0, 0);
         }
         fence_async_smem();
-        mbar_arrive(&b.z_full);
+        mbar_arrive(&b.z_full[zb]);
         ++n;
     }
 }
@@ -593,7 +604,7 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
                 }
         } else {   // columns contiguous over the rows
             const float* src = first ? q.start + (head * p.dz + t.slice * SL) * p.dr + r
-                                     : q.seg + ((head * p.nseg + o) * p.slices + t.slice) * (size_t)(SL * DRP) + r;
+                                     : segment_state<DRP>(p, t, o) + r;
             const int step = first ? p.dr : DRP, cols = first ? p.dz - t.slice * SL : SL;
 #pragma unroll
             for (int j = 0; j < SL; ++j)
@@ -628,20 +639,21 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
         if (t.count() == 0 && !writes_end) continue;
         start_state<DRP, STATES>(p, t, r, real, S);
         if (!STATES && t.count()) {
-            if (n > 0) ok = warp_wait(&b.s_free, (n - 1) & 1);
+            if (n > 0) ok = warp_wait(&b.o1_done[(n - 1) % K::STAGES], ((n - 1) / K::STAGES) & 1);
             if (ok) copy_state();
         }
         for (int i = 0; i < t.count(); ++i, ++n) {
             const int c = t.chunk(i), valid = t.valid(c);
-            ok = ok && warp_wait(&b.d_full, n & 1);
+            const uint32_t zb = n % K::BUF;
+            ok = ok && warp_wait(&b.d_done[n % K::STAGES], (n / K::STAGES) & 1);
             if (ok) {
                 tc_fence_after();
                 const float aC = linear::decay_pow(t.l2, valid);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     float hi[16], lo[16];
-                    tmem_ld16(tm + K::T_D + 16 * h + quarter, hi);
-                    tmem_ld16(tm + K::T_D + SL + 16 * h + quarter, lo);
+                    tmem_ld16(tm + K::T_D + zb * 2 * SL + 16 * h + quarter, hi);
+                    tmem_ld16(tm + K::T_D + zb * 2 * SL + SL + 16 * h + quarter, lo);
                     tmem_wait_ld(hi, lo);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {   // a^C S, then the small part, then the large one
@@ -652,17 +664,17 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&b.d_free);
+                mbar_arrive(&b.d_free[zb]);
             }
             if (!STATES && ok && i + 1 < t.count()) {
-                ok = warp_wait(&b.s_free, n & 1);
+                ok = warp_wait(&b.o1_done[n % K::STAGES], (n / K::STAGES) & 1);
                 if (ok) copy_state();
             }
             if (!ok) break;
         }
         if (!ok || !real) continue;
         if (STATES) {
-            float* dst = t.p->seg + ((((size_t)t.n * p.seq.H + t.h) * p.nseg + t.seg) * p.slices + t.slice) * (size_t)(SL * DRP) + r;
+            float* dst = segment_state<DRP>(p, t, t.seg) + r;
 #pragma unroll
             for (int j = 0; j < SL; ++j) dst[j * DRP] = S[j];
         } else if (writes_end && r < p.dr) {
@@ -684,17 +696,20 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     __shared__ __align__(16) float pw[256];
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < K::STAGES; ++s) {
-            mbar_init(&b.full[s], STATES ? 1 : 2);
-            mbar_init(&b.empty_x[s], 1); mbar_init(&b.empty_y[s], 1);
+        for (int i = 0; i < K::STAGES; ++i) {
+            mbar_init(&b.full[i], STATES ? 1 : 2);
+            mbar_init(&b.d_done[i], 1);
+            mbar_init(&b.o1_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.a_full[i], 1); mbar_init(&b.a_free[i], 1); mbar_init(&b.p_full[i], 128);
+            mbar_init(&b.a_full[i], 1);
+            mbar_init(&b.p_full[i], 128);
+            mbar_init(&b.o2_done[i], 1);
+            mbar_init(&b.z_full[i], 128);
+            mbar_init(&b.d_free[i], 128);
         }
-        mbar_init(&b.z_full, 128);
-        mbar_init(&b.o_full, 1); mbar_init(&b.o_free, 128);
-        mbar_init(&b.d_full, 1); mbar_init(&b.d_free, 128);
-        mbar_init(&b.s_full, 128); mbar_init(&b.s_free, 1);
+        mbar_init(&b.s_full, 128);
+        mbar_init(&b.o_free, 128);
         mbar_init(&b.drain, 1);
         fence_mbar_init();
     }
@@ -755,23 +770,36 @@ int sm_count() {
     return n;
 }
 
+// How a sequence's chunks are cut: segments of cps chunks, nseg of them at most, `slots` states for them all (and head
+// and slice).
 struct Cut {
     int nseg, cps;
+    long long slots;
 };
-// How a sequence's chunks are cut. Time in chunks of one block: the fullest block's chunks, 2 more for each item's
-// start and end, and for more than one segment the launch before (its chunks cost about 0.6 of a main one's, and the
-// launch itself 3).
-Cut choose_cut(const Seqs& s, int heads) {
+// Items of a call that is cut at all, at most: its workspace is sized by them (a packed call's lengths are not known then).
+long long most_items(long long heads) { return 2 * heads + 4 * sm_count(); }
+bool may_cut(const Seqs& s, long long heads) { return s.T > CT && heads < 4 * sm_count(); }
+// Time in chunks of one block: the fullest block's chunks, 2 more for each item's start and end, and for more than one
+// segment the launch before (its chunks cost about half a main one's, and the launch itself 3). Sequences of one length
+// go in waves; of packed ones only the sum of their lengths is known here, so the fullest block is taken to have the mean
+// and half an item more.
+Cut choose_cut(const Seqs& s, long long heads) {
     const int nc = (s.T + CT - 1) / CT, nsm = sm_count();
-    Cut best{1, std::max(nc, 1)};
+    Cut best{1, std::max(nc, 1), 0};
+    if (!may_cut(s, heads)) return best;
+    const double chunks = (s.Ttot / (double)CT + 0.5 * s.N) * ((double)heads / s.N);   // of packed sequences, over all heads
     double best_time = 1e30;
-    for (int r = 1; r <= 64 && r <= std::max(nc, 1); ++r) {
-        const int cps = std::max(1, (nc + r - 1) / r), nseg = std::max(1, (nc + cps - 1) / cps);
-        const double waves = (double)(((long long)heads * nseg + nsm - 1) / nsm);
-        const double t = waves * (cps + 2) + (nseg > 1 ? waves * (0.6 * cps + 2) + 3 : 0.0);
+    for (int r = 1; r <= 64 && r <= nc; ++r) {
+        const int cps = (nc + r - 1) / r, nseg = (nc + cps - 1) / cps;
+        const long long slots = s.Ttot / (cps * CT) + s.N + 1;
+        if (nseg > 1 && slots * (heads / s.N) > most_items(heads)) break;
+        const double waves = (double)((heads * nseg + nsm - 1) / nsm);
+        const double items = (double)heads + chunks / cps;
+        const double main = !s.cu ? waves * (cps + 2) : std::max(cps + 2.0, (chunks + 2 * items) / nsm + 0.5 * cps);
+        const double t = main + (nseg > 1 ? 0.5 * main + 3 : 0.0);
         if (t < best_time) {
             best_time = t;
-            best = Cut{nseg, cps};
+            best = Cut{nseg, cps, nseg > 1 ? slots : 0};
         }
     }
     return best;
@@ -781,7 +809,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int padded(int d) { return d > 64 ? 128 : 64; }
 int slices_of(int dz) { return (dz + SL - 1) / SL; }
 size_t seg_bytes(const Seqs& s, const Cut& c, int dr, int dz) {
-    return c.nseg > 1 ? align256((size_t)s.N * s.H * c.nseg * slices_of(dz) * SL * padded(dr) * sizeof(float)) : 0;
+    return align256((size_t)c.slots * s.H * slices_of(dz) * SL * padded(dr) * sizeof(float));
 }
 size_t state_bytes(const Seqs& s) { return align256((size_t)s.N * s.H * s.Dk * s.Dv * sizeof(float)); }
 
@@ -823,19 +851,18 @@ cudaError_t run_group(const LinearArgs& a, const Group& g, const Cut& cut, cudaS
 }
 
 // Passes of the forward (1) or the backward (3), as (row, value) sizes.
-int heads_of(const Seqs& s, bool bwd) {
+long long heads_of(const Seqs& s, bool bwd) {
     const int k = slices_of(s.Dk), v = slices_of(s.Dv);
-    return s.N * s.H * (bwd ? 2 * k + v : v);
+    return (long long)s.N * s.H * (bwd ? 2 * k + v : v);
 }
 
 }  // namespace
 
 size_t linear_chunk_workspace(const Seqs& s, bool bwd) {
-    if (s.T == 0) return 0;
-    const Cut c = choose_cut(s, heads_of(s, bwd));
-    const size_t keep = c.nseg > 1 ? state_bytes(s) : 0;   // a start state that the call's end state overwrites
-    if (!bwd) return keep + seg_bytes(s, c, s.Dk, s.Dv);
-    return keep + 2 * seg_bytes(s, c, s.Dv, s.Dk) + seg_bytes(s, c, s.Dk, s.Dv);
+    const long long heads = heads_of(s, bwd);
+    if (!may_cut(s, heads)) return 0;
+    // a start state that the call's end state overwrites, then the segments' states (each region 256-byte aligned)
+    return state_bytes(s) + (size_t)most_items(heads) * SL * padded(std::max(s.Dk, s.Dv)) * sizeof(float) + 3 * 256;
 }
 
 cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
