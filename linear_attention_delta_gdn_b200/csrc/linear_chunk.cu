@@ -779,10 +779,10 @@ struct Cut {
 // Items of a call that is cut at all, at most: its workspace is sized by them (a packed call's lengths are not known then).
 long long most_items(long long heads) { return 2 * heads + 4 * sm_count(); }
 bool may_cut(const Seqs& s, long long heads) { return s.T > CT && heads < 4 * sm_count(); }
-// Time in chunks of one block: the fullest block's chunks, 2 more for each item's start and end, and for more than one
-// segment the launch before (its chunks cost about half a main one's, and the launch itself 3). Sequences of one length
-// go in waves; of packed ones only the sum of their lengths is known here, so the fullest block is taken to have the mean
-// and half an item more.
+// Time in chunks of one block (2 us): the fullest block's chunks and 4 more for each of its items' start and end; for more
+// than one segment also the launch before, whose chunks cost half as much, and 3 for the launch itself. Sequences of one
+// length go in waves. Of packed ones only the sum of their lengths is known here: the fullest block is taken to have the
+// mean and half an item more, and an item without chunks costs 1.
 Cut choose_cut(const Seqs& s, long long heads) {
     const int nc = (s.T + CT - 1) / CT, nsm = sm_count();
     Cut best{1, std::max(nc, 1), 0};
@@ -794,9 +794,12 @@ Cut choose_cut(const Seqs& s, long long heads) {
         const long long slots = s.Ttot / (cps * CT) + s.N + 1;
         if (nseg > 1 && slots * (heads / s.N) > most_items(heads)) break;
         const double waves = (double)((heads * nseg + nsm - 1) / nsm);
-        const double items = (double)heads + chunks / cps;
-        const double main = !s.cu ? waves * (cps + 2) : std::max(cps + 2.0, (chunks + 2 * items) / nsm + 0.5 * cps);
-        const double t = main + (nseg > 1 ? 0.5 * main + 3 : 0.0);
+        const double items = 0.5 * heads + chunks / cps, empty = std::max(0.0, (double)heads * nseg - items);
+        auto time = [&](double chunk) {
+            return !s.cu ? waves * (chunk * cps + 4)
+                         : std::max(chunk * cps + 4, (chunk * chunks + 4 * items + empty) / nsm + 0.5 * (chunk * cps + 4));
+        };
+        const double t = time(1.0) + (nseg > 1 ? time(0.5) + 3 : 0.0);
         if (t < best_time) {
             best_time = t;
             best = Cut{nseg, cps, nseg > 1 ? slots : 0};
@@ -824,7 +827,9 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     using K = Cfg<DRP, STATES>;
     cudaError_t e = cudaFuncSetAttribute(linear_chunk_kernel<DRP, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::SMEM);
     if (e != cudaSuccess) return e;
-    const int grid = std::min(p.items, sm_count());
+    // Items of one length are taken in turn by one block an SM. A cut packed call's are not, and many are empty: there each
+    // has a block of its own, and the hardware hands out the next one to the SM that gets free.
+    const int grid = p.seq.cu && p.nseg > 1 ? p.items : std::min(p.items, sm_count());
     TraceScope trace(STATES ? K_LINEAR_SEGMENT : K_LINEAR_CHUNK, s);
     linear_chunk_kernel<DRP, STATES><<<grid, NT, K::SMEM, s>>>(p);
     return cudaGetLastError();
