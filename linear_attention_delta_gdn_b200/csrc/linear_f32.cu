@@ -45,7 +45,9 @@ struct WarpTiles {
     static_assert(MT * WM == MALL && NT * WN == NALL, "tiles must divide");
 };
 
-// acc += A B for this warp's tiles; a(m, k) and b(k, n) give the operands' elements.
+// acc += A B for this warp's tiles; a(m, k) and b(k, n) give the operands' elements. Eight products a time are summed by
+// the tensor core from zero and added to acc in 32 bits: its own accumulation cuts bits off instead of rounding, which
+// over a long sum would add up.
 template <int M, int N, int K, typename FA, typename FB>
 __device__ __forceinline__ void warp_gemm(float (&acc)[WarpTiles<M, N>::MT][WarpTiles<M, N>::NT][4], FA a, FB b) {
     using W = WarpTiles<M, N>;
@@ -67,9 +69,12 @@ __device__ __forceinline__ void warp_gemm(float (&acc)[WarpTiles<M, N>::MT][Warp
             for (int e = 0; e < 2; ++e) split(b(k0 + t + 4 * e, n0 + 8 * j + g), &bb[e], &bs[e]);
 #pragma unroll
             for (int i = 0; i < W::MT; ++i) {
-                chunk::mma_tf32_16x8x8(acc[i][j], as[i][0], as[i][1], as[i][2], as[i][3], bb[0], bb[1]);
-                chunk::mma_tf32_16x8x8(acc[i][j], ab[i][0], ab[i][1], ab[i][2], ab[i][3], bs[0], bs[1]);
-                chunk::mma_tf32_16x8x8(acc[i][j], ab[i][0], ab[i][1], ab[i][2], ab[i][3], bb[0], bb[1]);
+                float d[4] = {};
+                chunk::mma_tf32_16x8x8(d, as[i][0], as[i][1], as[i][2], as[i][3], bb[0], bb[1]);
+                chunk::mma_tf32_16x8x8(d, ab[i][0], ab[i][1], ab[i][2], ab[i][3], bs[0], bs[1]);
+                chunk::mma_tf32_16x8x8(d, ab[i][0], ab[i][1], ab[i][2], ab[i][3], bb[0], bb[1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] += d[e];
             }
         }
     }
@@ -194,7 +199,7 @@ struct OutJob {
     int rev, transposed;   // transposed: the state is read as [DZ][DR]
 };
 struct OutJobs {
-    OutJob job[2];
+    OutJob job[3];
 };
 
 template <int DR, int DZ>
@@ -279,8 +284,13 @@ cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
     }
     oj.job[0] = OutJob{a.dout, a.v, a.k, w, a.dq, 0, 1};
     oj.job[1] = OutJob{a.v, a.dout, a.q, w + set, a.dk, 1, 1};
+    const OutJob dv{a.k, a.q, a.dout, w + set, a.dv, 1, 0};
+    if constexpr (DK == DV) {   // one kernel shape: one launch
+        oj.job[2] = dv;
+        return outputs<DK, DV>(a, nc, oj, 3, s);
+    }
     if ((e = outputs<DV, DK>(a, nc, oj, 2, s)) != cudaSuccess) return e;
-    oj.job[0] = OutJob{a.k, a.q, a.dout, w + set, a.dv, 1, 0};
+    oj.job[0] = dv;
     return outputs<DK, DV>(a, nc, oj, 1, s);
 }
 
