@@ -95,17 +95,24 @@ __device__ __forceinline__ void each_element(float (&acc)[WarpTiles<M, N>::MT][W
             for (int e = 0; e < 4; ++e) f(m0 + 16 * i + g + 8 * (e >> 1), n0 + 8 * j + 2 * t + (e & 1), acc[i][j][e]);
 }
 
-// One chunk's rows of a token tensor into shared memory as floats, zeros behind the chunk's last token (the rows
+// One chunk's rows of a token tensor on their way into shared memory, zeros behind the chunk's last token (the rows
 // there may be another sequence's).
 template <int D, int LD>
-__device__ __forceinline__ void load_rows(float* dst, const float* src, long long row0, int valid, int H, int h) {
+__device__ __forceinline__ void load_rows(float* dst, const void* src, long long row0, int valid, int H, int h) {
     constexpr int PER = D / 4;
     for (int x = threadIdx.x; x < C32 * PER; x += NT32) {
         const int r = x / PER, p = x % PER;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < valid) v = *reinterpret_cast<const float4*>(src + ((size_t)(row0 + r) * H + h) * D + 4 * p);
-        *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = v;
+        if (r < valid)
+            tc::cp_async16_cg(dst + r * LD + 4 * p, static_cast<const float*>(src) + ((size_t)(row0 + r) * H + h) * D + 4 * p);
+        else
+            *reinterpret_cast<float4*>(dst + r * LD + 4 * p) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+}
+// A matrix of R rows of D, the same way.
+template <int R, int D, int LD>
+__device__ __forceinline__ void load_state(float* dst, const float* src) {
+    constexpr int PER = D / 4;
+    for (int x = threadIdx.x; x < R * PER; x += NT32) tc::cp_async16_cg(dst + (x / PER) * LD + 4 * (x % PER), src + 4 * x);
 }
 struct Unit {
     int n, h, c, len, valid;
@@ -145,13 +152,14 @@ __global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, cons
     Unit u;
     if (!unit_of(s, nc, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
-    load_rows<DK, LY>(Y, static_cast<const float*>(job.y), u.row0, u.valid, s.H, u.h);
-    load_rows<DV, LZ>(Z, static_cast<const float*>(job.z), u.row0, u.valid, s.H, u.h);
+    load_rows<DK, LY>(Y, job.y, u.row0, u.valid, s.H, u.h);
+    load_rows<DV, LZ>(Z, job.z, u.row0, u.valid, s.H, u.h);
     __shared__ float f[C32];
     if (threadIdx.x < C32) {
         const int j = threadIdx.x;
         f[j] = j < u.valid ? linear::decay_pow(l2, job.rev ? j + 1 : u.valid - 1 - j) : 0.f;
     }
+    tc::cp_async_wait_all();
     __syncthreads();
     float acc[WarpTiles<DK, DV>::MT][WarpTiles<DK, DV>::NT][4] = {};
     warp_gemm<DK, DV, C32>(acc, [&](int m, int k) { return Y[k * LY + m]; }, [&](int k, int n) { return Z[k * LZ + n] * f[k]; });
@@ -202,35 +210,51 @@ struct OutJobs {
     OutJob job[3];
 };
 
+// Shared memory of a block: all operands at once, so that every load is under way from the start. P takes the place of Y.
+template <int DR, int DZ>
+struct OutTiles {
+    static constexpr int LX = DR + 4, LZ = DZ + 8, LP = C32 + 4;   // shifts a row: fragment reads meet no bank twice
+    static constexpr int Y = C32 * LX, Z = Y + C32 * (LX > LP ? LX : LP), S = Z + C32 * LZ;
+    static constexpr int FLOATS = S + (DR * LZ > DZ * LX ? DR * LZ : DZ * LX);
+};
+
 template <int DR, int DZ>
 __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const float* __restrict__ log_decay, OutJobs jobs) {
-    constexpr int LX = DR + 4, LZ = DZ + 8, LP = C32 + 4;
+    using L = OutTiles<DR, DZ>;
+    constexpr int LX = L::LX, LZ = L::LZ, LP = L::LP;
     extern __shared__ float sm[];
-    float *X = sm, *Y = X + C32 * LX, *Z = Y + C32 * LX, *P = Z + C32 * LZ;
+    float *X = sm, *Y = sm + L::Y, *Z = sm + L::Z, *S = sm + L::S, *P = Y;
     __shared__ float pw[C32 + 1];
     const OutJob& job = jobs.job[blockIdx.y];
     Unit u;
     if (!unit_of(s, nc, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
-    load_rows<DR, LX>(X, static_cast<const float*>(job.x), u.row0, u.valid, s.H, u.h);
-    load_rows<DR, LX>(Y, static_cast<const float*>(job.y), u.row0, u.valid, s.H, u.h);
-    load_rows<DZ, LZ>(Z, static_cast<const float*>(job.z), u.row0, u.valid, s.H, u.h);
-    if (threadIdx.x <= C32) pw[threadIdx.x] = linear::decay_pow(l2, threadIdx.x);
-    __syncthreads();
-    {
-        float p[WarpTiles<C32, C32>::MT][WarpTiles<C32, C32>::NT][4] = {};
-        warp_gemm<C32, C32, DR>(p, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return Y[n * LX + k]; });
-        each_element<C32, C32>(p, [&](int m, int n, float x) {
-            const int far = job.rev ? n - m : m - n;
-            P[m * LP + n] = far >= 0 ? x * pw[far] : 0.f;
-        });
-    }
-    float acc[WarpTiles<C32, DZ>::MT][WarpTiles<C32, DZ>::NT][4] = {};
-    const float* S = job.states + (size_t)u.state * DR * DZ;
+    const float* state = job.states + (size_t)u.state * DR * DZ;
+    load_rows<DR, LX>(X, job.x, u.row0, u.valid, s.H, u.h);
+    load_rows<DR, LX>(Y, job.y, u.row0, u.valid, s.H, u.h);
+    tc::cp_async_commit();
     if (job.transposed)
-        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return __ldg(S + n * DR + k); });
+        load_state<DZ, DR, LX>(S, state);
     else
-        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return __ldg(S + k * DZ + n); });
+        load_state<DR, DZ, LZ>(S, state);
+    load_rows<DZ, LZ>(Z, job.z, u.row0, u.valid, s.H, u.h);
+    tc::cp_async_commit();
+    if (threadIdx.x <= C32) pw[threadIdx.x] = linear::decay_pow(l2, threadIdx.x);
+    tc::cp_async_wait_but1();
+    __syncthreads();
+    float p[WarpTiles<C32, C32>::MT][WarpTiles<C32, C32>::NT][4] = {};
+    warp_gemm<C32, C32, DR>(p, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return Y[n * LX + k]; });
+    tc::cp_async_wait_all();
+    __syncthreads();
+    each_element<C32, C32>(p, [&](int m, int n, float x) {
+        const int far = job.rev ? n - m : m - n;
+        P[m * LP + n] = far >= 0 ? x * pw[far] : 0.f;
+    });
+    float acc[WarpTiles<C32, DZ>::MT][WarpTiles<C32, DZ>::NT][4] = {};
+    if (job.transposed)
+        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return S[n * LX + k]; });
+    else
+        warp_gemm<C32, DZ, DR>(acc, [&](int m, int k) { return X[m * LX + k]; }, [&](int k, int n) { return S[k * LZ + n]; });
     each_element<C32, DZ>(acc, [&](int m, int, float& x) { x *= m < u.valid ? pw[job.rev ? u.valid - 1 - m : m + 1] : 0.f; });
     __syncthreads();
     warp_gemm<C32, DZ, C32>(acc, [&](int m, int k) { return P[m * LP + k]; }, [&](int k, int n) { return Z[k * LZ + n]; });
@@ -253,7 +277,7 @@ cudaError_t states(const LinearArgs& a, int nc, const StateJobs& jobs, int n, cu
 }
 template <int DR, int DZ>
 cudaError_t outputs(const LinearArgs& a, int nc, const OutJobs& jobs, int n, cudaStream_t s) {
-    const int smem = (int)sizeof(float) * C32 * (2 * (DR + 4) + DZ + 8 + C32 + 4);
+    const int smem = (int)sizeof(float) * OutTiles<DR, DZ>::FLOATS;
     cudaError_t e = cudaFuncSetAttribute(chunk_out_kernel<DR, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TraceScope trace(K_LINEAR_OUT, s);
