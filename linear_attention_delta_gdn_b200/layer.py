@@ -68,3 +68,65 @@ class Gdn2Layer(torch.nn.Module):
         o, ST = binding.gated_delta_rule2(q, k, v, la, b, w, S0, self.chunk)
         y = o.reshape(B, T, self.H * self.Dv) @ self.W_out
         return y, ST
+
+
+class DecayLinearAttentionLayer(torch.nn.Module):
+    """A linear-attention layer with one fixed decay per head:
+
+        q, k = x W_qk per head,  RMS-normalised with a weight each, pairs of channels turned by the token's position
+        v = x W_v;   o, S_T = linear attention (q, k, v, log_decay, S0);   y = o W_out
+
+    ``y, S_T = layer(x, S0, positions)`` for x [B, T, d_model], or packed [Ttot, d_model] with ``cu_seqlens`` and ``Tmax``;
+    ``layer.step(x, positions, S, slots)`` for one token of each of B requests. ``pairs`` (d_k / 2 if not given) channel
+    pairs turn; with ``sections`` pair by pair along several axes, positions then being [axes, ...]. ``log_decay`` [n_heads]
+    defaults to memories of 8 to 256 tokens. bf16 or fp32.
+    """
+
+    def __init__(self, d_model: int, n_heads: int, d_k: int = 128, d_v: int = 128, pairs: Optional[int] = None, sections=None,
+                 base: float = 10000.0, eps: float = 1e-6, log_decay: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
+                 device=None):
+        super().__init__()
+        self.d_model, self.H, self.Dk, self.Dv, self.eps = d_model, n_heads, d_k, d_v, eps
+        pairs = pairs or (sum(sections) if sections else d_k // 2)
+        if sections and sum(sections) != pairs:
+            raise ValueError("sections %s do not add up to %d pairs" % (list(sections), pairs))
+        rand = lambda m, n: torch.nn.Parameter(torch.randn(m, n, device=device).div_(math.sqrt(m)).to(dtype))
+        self.W_qk, self.W_v, self.W_out = rand(d_model, 2 * n_heads * d_k), rand(d_model, n_heads * d_v), rand(n_heads * d_v, d_model)
+        # products of normalised queries and keys start at a variance of one
+        self.q_weight = torch.nn.Parameter(torch.full((d_k,), 1 / math.sqrt(d_k), device=device))
+        self.k_weight = torch.nn.Parameter(torch.ones(d_k, device=device))
+        if log_decay is None:
+            log_decay = -torch.exp2(-torch.linspace(3, 8, n_heads))
+        self.register_buffer("log_decay", log_decay.to(device=device, dtype=torch.float32))
+        self.register_buffer("inv_freq", (base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)).float().to(device))
+        self.register_buffer("axes", binding.rope_axes(sections, device or "cpu") if sections else None)
+
+    def _qkv(self, x, positions):
+        """x [B, T, d_model], positions [B, T] or [axes, B, T]: normalised and turned q, k, and v, [B, T, H, D] each."""
+        B, T, _ = x.shape
+        q, k = (t.view(B, T, self.H, self.Dk) for t in (x @ self.W_qk).split(self.H * self.Dk, -1))
+        q, k = binding.qk_norm_rope(q, k, positions, self.inv_freq, self.axes, self.q_weight, self.k_weight, self.eps)
+        return q, k, (x @ self.W_v).view(B, T, self.H, self.Dv)
+
+    def forward(self, x, S0: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                cu_seqlens: Optional[torch.Tensor] = None, Tmax: Optional[int] = None):
+        packed = cu_seqlens is not None
+        if positions is None:
+            if packed or self.axes is not None:
+                raise ValueError("positions are needed with packed sequences and with several axes")
+            positions = torch.arange(x.shape[1], dtype=torch.int32, device=x.device).expand(x.shape[:2]).contiguous()
+        if not packed:
+            q, k, v = self._qkv(x, positions)
+            o, ST = binding.decay_linear_attention(q, k, v, self.log_decay, S0)
+        else:
+            q, k, v = self._qkv(x[None], positions.unsqueeze(-2))
+            o, ST = binding.decay_linear_attention(q[0], k[0], v[0], self.log_decay, S0, cu_seqlens, Tmax)
+        return o.flatten(-2) @ self.W_out, ST
+
+    @torch.no_grad()
+    def step(self, x, positions, S, slots: Optional[torch.Tensor] = None):
+        """y [B, d_model] for one token of each request: x [B, d_model], positions [B] or [axes, B]; S [num_slots, H, Dk,
+        Dv] fp32 is updated in place at ``slots`` (int32 [B]; negative: an idle row)."""
+        q, k, v = self._qkv(x[:, None], positions.unsqueeze(-1))
+        o = binding.gdn2_linear_decode_step(q[:, 0], k[:, 0], v[:, 0], self.log_decay, S, slots)
+        return o.flatten(-2) @ self.W_out

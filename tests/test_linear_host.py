@@ -222,3 +222,18 @@ def test_rotation_argument_checks():
     with pytest.raises(TypeError):
         check(p=pos.float())
     assert b.rope_axes((2, 3, 3), "cpu").tolist() == [0, 0, 1, 1, 1, 2, 2, 2]
+
+
+def test_layer_refusals():
+    from linear_attention_delta_gdn_b200.layer import DecayLinearAttentionLayer
+    with pytest.raises(ValueError, match="add up"):
+        DecayLinearAttentionLayer(32, 2, 16, 16, pairs=8, sections=(2, 3))
+    layer = DecayLinearAttentionLayer(32, 2, 16, 16, sections=(3, 5), dtype=torch.float32)
+    assert layer.axes.tolist() == [0] * 3 + [1] * 5 and layer.inv_freq.shape == (8,)
+    with pytest.raises(ValueError, match="positions"):
+        layer(torch.zeros(1, 4, 32))
+    layer = DecayLinearAttentionLayer(32, 2, 16, 16, dtype=torch.float32)
+    with pytest.raises(ValueError, match="positions"):
+        layer(torch.zeros(4, 32), cu_seqlens=torch.tensor([0, 4], dtype=torch.int32), Tmax=4)
+    with pytest.raises(ValueError, match="CUDA"):
+        layer(torch.zeros(1, 4, 32))
