@@ -489,23 +489,27 @@ __device__ __forceinline__ void two_terms(uint32_t z2, __nv_bfloat162 gh, __nv_b
 }
 
 // Z does not come through TMA: its rows go from global memory to registers a chunk ahead (eight lanes a row), and from
-// there to shared memory as they are and as the two terms. Nothing then waits for a stage to be given back.
+// there to shared memory as they are and as the two terms. Nothing then waits for a stage to be given back. Where only
+// states are made, two warpgroups take the chunks, and the two buffers, in turn (`share`).
 template <int DRP, bool STATES>
-__device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
+__device__ void split_values(const Params& p, unsigned char* sm, Bars& b, uint32_t share) {
     using K = Cfg<DRP, STATES>;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
     const int r0 = 32 * w + (lane >> 3), c = lane & 7;   // rows r0 + 4 k, 16-byte piece c
-    uint32_t n = 0;
+    uint32_t n = 0xffffffffu;                            // chunks so far, over items
     Item t;
     int x = blockIdx.x, i = -1;
-    auto next = [&]() {   // to the next chunk, over items; false behind the last
-        ++i;
-        if (n == 0 && i == 0 && x < p.items) t = item_of<STATES>(p, x);
-        while (x < p.items && i >= t.count()) {
-            x += gridDim.x;
-            i = 0;
-            if (x < p.items) t = item_of<STATES>(p, x);
-        }
+    if (x < p.items) t = item_of<STATES>(p, x);
+    auto next = [&]() {   // to this warpgroup's next chunk, over items; false behind the last
+        do {
+            ++n;
+            ++i;
+            while (x < p.items && i >= t.count()) {
+                x += gridDim.x;
+                i = 0;
+                if (x < p.items) t = item_of<STATES>(p, x);
+            }
+        } while (STATES && x < p.items && (n & 1) != share);
         return x < p.items;
     };
     uint4 ahead[8];
@@ -522,6 +526,7 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
     __nv_bfloat162 gh[8], gl[8];   // the rows' weights
     int have = -1, have_x = -1;
     while (more) {
+        const uint32_t m = n, zb = m % K::BUF, back = m - K::BUF;
         const int valid = t.valid(t.chunk(i));
         const float l2 = t.l2;
         const bool rev = t.p->rev;
@@ -542,10 +547,9 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
         more = next();
         if (more) load();
         // Zh and Zl are free once the D that read them is done, this copy of Z once the chunk before that has its O2
-        const uint32_t zb = n % K::BUF, m = n - K::BUF;
-        if (n >= (uint32_t)K::BUF && !warp_wait(&b.d_done[m % K::STAGES], (m / K::STAGES) & 1)) return;
-        if (!STATES && !warp_wait(&b.o2_done[n & 1], ((n >> 1) & 1) ^ 1)) return;
-        unsigned char* Z = sm + K::OFF_Z + (n & 1) * K::ZB;
+        if (m >= (uint32_t)K::BUF && !warp_wait(&b.d_done[back % K::STAGES], (back / K::STAGES) & 1)) return;
+        if (!STATES && !warp_wait(&b.o2_done[m & 1], ((m >> 1) & 1) ^ 1)) return;
+        unsigned char* Z = sm + K::OFF_Z + (m & 1) * K::ZB;
         unsigned char *Zh = sm + K::OFF_ZH + zb * 2 * K::ZB, *Zl = Zh + K::ZB;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -560,8 +564,8 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
             if (!STATES) *reinterpret_cast<uint4*>(Z + at) = z[k];
         }
         if (valid < CT) {   // rows of Y behind the sequence's end: they are another's, and would meet the zeros of Z
-            const uint32_t s = n % K::STAGES;
-            if (!warp_wait(&b.full[s], (n / K::STAGES) & 1)) return;
+            const uint32_t s = m % K::STAGES;
+            if (!warp_wait(&b.full[s], (m / K::STAGES) & 1)) return;
             if (tid >= valid)
 #pragma unroll 1
                 for (int q = 0; q < DRP / 8; ++q)
@@ -569,7 +573,6 @@ __device__ void split_values(const Params& p, unsigned char* sm, Bars& b) {
         }
         fence_async_smem();
         mbar_arrive(&b.z_full[zb]);
-        ++n;
     }
 }
 
@@ -733,9 +736,9 @@ __global__ void __launch_bounds__(NT, 1) linear_chunk_kernel(const __grid_consta
     } else if (warp == 1) {
         if (elect_one()) issue_products<DRP, STATES>(p, sm, tm, b);
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (!STATES && warp >= 4 && warp < 8) {
         if constexpr (!STATES) weigh_pairs<DRP>(p, sm, tm, b, pw);
-    } else if (warp >= 8 && warp < 12) split_values<DRP, STATES>(p, sm, b);
+    } else if (warp >= 4 && warp < 12) split_values<DRP, STATES>(p, sm, b, warp >= 8);
     else if (warp >= 12) carry_state<DRP, STATES>(p, sm, tm, b);
     tc_fence_before();
     __syncthreads();
@@ -779,27 +782,33 @@ struct Cut {
 // Items of a call that is cut at all, at most: its workspace is sized by them (a packed call's lengths are not known then).
 long long most_items(long long heads) { return 2 * heads + 4 * sm_count(); }
 bool may_cut(const Seqs& s, long long heads) { return s.T > CT && heads < 4 * sm_count(); }
-// Time in chunks of one block (2 us): the fullest block's chunks and 4 more for each of its items' start and end; for more
-// than one segment also the launch before, whose chunks cost half as much, and 3 for the launch itself. Sequences of one
-// length go in waves. Of packed ones only the sum of their lengths is known here: the fullest block is taken to have the
-// mean and half an item more, and an item without chunks costs 1.
+// Time in chunks of one block (1.9 us): the fullest block's chunks and 4 more for each of its items' start and end, in
+// more than one segment also 1.5 for each segment that an item's start is summed from, and the launch before, whose chunks
+// cost half as much (a sequence's last segment has none there), with 3 for the launch itself. Sequences of one length go in
+// waves. Of packed ones only the sum of their lengths is known here: the fullest block is taken to have the mean and half
+// an item more, and an item without chunks costs 1. One sequence of 65536 tokens, 16 heads of 128: 951 us uncut, 675 / 465 /
+// 381 us in 2 / 3 / 4 segments (one wave), 403 us in 9 (two waves), 564 us in 5 (two waves, the second nearly empty). Eight
+// packed sequences of 12557 tokens in all, 8 heads of 64 x 128: 91 us uncut, 85 us in 2 or 3 segments, 105 us in 6.
 Cut choose_cut(const Seqs& s, long long heads) {
     const int nc = (s.T + CT - 1) / CT, nsm = sm_count();
     Cut best{1, std::max(nc, 1), 0};
     if (!may_cut(s, heads)) return best;
-    const double chunks = (s.Ttot / (double)CT + 0.5 * s.N) * ((double)heads / s.N);   // of packed sequences, over all heads
+    const double total = (s.Ttot / (double)CT + 0.5 * s.N) * ((double)heads / s.N);   // packed chunks, over all heads
     double best_time = 1e30;
     for (int r = 1; r <= 64 && r <= nc; ++r) {
         const int cps = (nc + r - 1) / r, nseg = (nc + cps - 1) / cps;
         const long long slots = s.Ttot / (cps * CT) + s.N + 1;
         if (nseg > 1 && slots * (heads / s.N) > most_items(heads)) break;
-        const double waves = (double)((heads * nseg + nsm - 1) / nsm);
-        const double items = 0.5 * heads + chunks / cps, empty = std::max(0.0, (double)heads * nseg - items);
-        auto time = [&](double chunk) {
-            return !s.cu ? waves * (chunk * cps + 4)
-                         : std::max(chunk * cps + 4, (chunk * chunks + 4 * items + empty) / nsm + 0.5 * (chunk * cps + 4));
+        // a launch's time from the cost of a chunk and of an item, its segments a sequence, and of packed sequences its
+        // chunks and its items with chunks
+        auto time = [&](double chunk, double item, int segs, double chunks, double items) {
+            const double one = chunk * cps + item;
+            if (!s.cu) return (double)((heads * segs + nsm - 1) / nsm) * one;
+            return std::max(one, (chunk * chunks + 4 * items + std::max(0.0, (double)heads * nseg - items)) / nsm + 0.5 * one);
         };
-        const double t = time(1.0) + (nseg > 1 ? time(0.5) + 3 : 0.0);
+        const double items = 0.5 * heads + total / cps;
+        double t = time(1.0, 4 + 1.5 * (nseg - 1), nseg, total, items);
+        if (nseg > 1) t += time(0.5, 4, nseg - 1, std::max(0.0, total - 0.5 * heads * cps), std::max(0.0, items - heads)) + 3;
         if (t < best_time) {
             best_time = t;
             best = Cut{nseg, cps, nseg > 1 ? slots : 0};
@@ -872,13 +881,7 @@ size_t linear_chunk_workspace(const Seqs& s, bool bwd) {
 
 cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
     const Seqs& q = a.seq;
-    if (q.T == 0) {   // no tokens: the state is handed on
-        float* end = bwd ? a.dS0 : a.ST;
-        const float* start = bwd ? a.dST : a.S0;
-        const size_t bytes = (size_t)q.N * q.H * q.Dk * q.Dv * sizeof(float);
-        if (!end || end == start) return cudaSuccess;
-        return start ? cudaMemcpyAsync(end, start, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(end, 0, bytes, s);
-    }
+    if (q.T == 0) return linear32_launch(a, bwd, s);   // no tokens: states alone are handed on (and cu_seqlens checked)
     const Cut cut = choose_cut(q, heads_of(q, bwd));
     unsigned char* w = static_cast<unsigned char*>(a.ws);
     const float *S0 = a.S0, *dST = a.dST;
