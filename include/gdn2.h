@@ -363,7 +363,7 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
  *                        and dS0 dST.
  * gdn2_linear_bwd gives the gradients of <dout, o> + <dST, S_T> from the
  * forward's inputs alone (nothing is kept by the forward); the three token
- * gradients must be given and must not alias the inputs.
+ * gradients must be given. o and the token gradients must not alias the inputs.
  * Dk, Dv in {16, 32, 64, 128}, float32 or bf16, any T >= 0.
  * NaN and infinity in a token reach every output of the chunk of 128 tokens it
  * lies in, earlier ones too, and the states behind it (before it, for the

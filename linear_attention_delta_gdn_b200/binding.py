@@ -427,16 +427,19 @@ def gdn2_decode_step(q, k, v, log_alpha, b, w, S, o=None):
 
 # ------------------------------------------------------------------ linear attention with a decay per head
 
-def _on(t: torch.Tensor, device, name: str):
+# A call of one token takes the GPU a few microseconds, so the checks of these calls are made of cheap questions: a
+# tensor's device by index, shapes read once.
+
+def _on(t: torch.Tensor, device: int, name: str) -> int:
     """Device pointer of a contiguous tensor on the call's device (as an int: ctypes converts it by the argtypes)."""
-    if t.device != device:
-        raise ValueError("%s must be on %s, not on %s" % (name, device, t.device))
+    if t.get_device() != device:
+        raise ValueError("%s must be on cuda:%d, not on %s" % (name, device, t.device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _opt(t: Optional[torch.Tensor], device, name: str, dtype, shape):
+def _opt(t: Optional[torch.Tensor], device: int, name: str, dtype, shape):
     if t is None:
         return None
     if t.dtype != dtype or t.shape != shape:
@@ -446,17 +449,18 @@ def _opt(t: Optional[torch.Tensor], device, name: str, dtype, shape):
 
 # the current stream's handle without the Stream object around it, which costs more than a launch
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _here(t: torch.Tensor, call):
     """``call(device, stream)`` with t's device current (launches go to the current device) and its current stream."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    dev = t.device
-    if dev.index == torch.cuda.current_device():
-        return call(dev, _raw_stream(dev.index))
+    dev = t.get_device()
+    if dev == _current_device():
+        return call(dev, _raw_stream(dev))
     with torch.cuda.device(dev):
-        return call(dev, _raw_stream(dev.index))
+        return call(dev, _raw_stream(dev))
 
 
 def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int, dt: int) -> int:
@@ -466,17 +470,18 @@ def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int
 def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs, ends):
     """Shared by the four whole-sequence calls: checks, outputs, workspace, the call. Returns (outs, end state)."""
     packed = cu is not None
-    if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
+    qs, vs = q.shape, v.shape
+    if len(qs) != (3 if packed else 4) or len(vs) != len(qs):
         raise ValueError("q and v must be [%sH, D]" % ("Ttot, " if packed else "B, T, "))
-    *lead, H, Dk = q.shape
-    Dv = v.shape[-1]
+    *lead, H, Dk = qs
+    Dv = vs[-1]
     dt, code = q.dtype, _dt(q)
-    if k.dtype != dt or k.shape != q.shape:
-        raise ValueError("k must be %s %s" % (dt, list(q.shape)))
-    if v.dtype != dt or v.shape[:-1] != q.shape[:-1]:
+    if k.dtype != dt or k.shape != qs:
+        raise ValueError("k must be %s %s" % (dt, list(qs)))
+    if v.dtype != dt or vs[:-1] != qs[:-1]:
         raise ValueError("v must be %s %s" % (dt, lead + [H, "Dv"]))
-    if dout is not None and (dout.dtype != dt or dout.shape != v.shape):
-        raise ValueError("dout must be %s %s" % (dt, list(v.shape)))
+    if dout is not None and (dout.dtype != dt or dout.shape != vs):
+        raise ValueError("dout must be %s %s" % (dt, list(vs)))
     if log_decay.dtype != torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != H:
         raise ValueError("log_decay must be float32 [%d]" % H)
     if packed:
@@ -491,10 +496,11 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
 
     def call(dev, stream):
         nonlocal ws
+        args = [_on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay")]
         made = []
-        for name, t, like in outs:
+        for name, t, like in outs:   # (contiguous, as q, k and v are)
             if t is None:
-                t = torch.empty_like(like, memory_format=torch.contiguous_format)
+                t = torch.empty_like(like)
             elif t.dtype != dt or t.shape != like.shape:
                 raise ValueError("%s must be %s %s" % (name, dt, list(like.shape)))
             made.append(t)
@@ -505,7 +511,6 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
         need = L.gdn2_linear_workspace_size(GDN2_OP_BWD if bwd else GDN2_OP_FWD, N, T, H, Dk, Dv, code)
         if ws is None and need:
             ws = q.new_empty(need, dtype=torch.uint8)
-        args = [_on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay")]
         if packed:
             args += [_on(cu, dev, "cu_seqlens"), N, T, lead[0]]
         args.append(_opt(S0, dev, "S0", f32, state))
@@ -570,25 +575,27 @@ def gdn2_linear_decode_step(q, k, v, log_decay, S, slots=None, o=None):
     """One token of :func:`gdn2_linear_fwd` for every row: q, k, v [B, H, D]; S [num_slots, H, Dk, Dv] fp32, updated in
     place. ``slots`` (int32 [B] on the device) names each row's state, a negative one an idle row (its o is zero);
     None: row b has S[b]. Returns o."""
-    if q.dim() != 3 or v.dim() != 3:
+    qs, vs, ss = q.shape, v.shape, S.shape
+    if len(qs) != 3 or len(vs) != 3:
         raise ValueError("q and v must be [B, H, D]")
-    B, H, Dk = q.shape
-    Dv = v.shape[-1]
+    B, H, Dk = qs
+    Dv = vs[2]
     dt, code = q.dtype, _dt(q)
-    if k.dtype != dt or k.shape != q.shape or v.dtype != dt or v.shape[:2] != q.shape[:2]:
+    if k.dtype != dt or k.shape != qs or v.dtype != dt or vs[0] != B or vs[1] != H:
         raise ValueError("k and v must be %s [%d, %d, D]" % (dt, B, H))
     if log_decay.dtype != torch.float32 or log_decay.dim() != 1 or log_decay.shape[0] != H:
         raise ValueError("log_decay must be float32 [%d]" % H)
-    if S.dtype != torch.float32 or S.dim() != 4 or S.shape[1:] != (H, Dk, Dv):
+    if S.dtype != torch.float32 or len(ss) != 4 or ss[1] != H or ss[2] != Dk or ss[3] != Dv:
         raise ValueError("S must be float32 [num_slots, %d, %d, %d]" % (H, Dk, Dv))
-    if o is not None and (o.dtype != dt or o.shape != v.shape):
+    if o is not None and (o.dtype != dt or o.shape != vs):
         raise ValueError("o must be %s [%d, %d, %d]" % (dt, B, H, Dv))
 
     def call(dev, stream):
-        out = torch.empty_like(v, memory_format=torch.contiguous_format) if o is None else o
+        vp = _on(v, dev, "v")
+        out = torch.empty_like(v) if o is None else o
         rc = lib().gdn2_linear_decode_step(
-            _on(q, dev, "q"), _on(k, dev, "k"), _on(v, dev, "v"), _on(log_decay, dev, "log_decay"), _on(S, dev, "S"),
-            _opt(slots, dev, "slots", torch.int32, (B,)), S.shape[0], _on(out, dev, "o"), B, H, Dk, Dv, code, stream)
+            _on(q, dev, "q"), _on(k, dev, "k"), vp, _on(log_decay, dev, "log_decay"), _on(S, dev, "S"),
+            _opt(slots, dev, "slots", torch.int32, (B,)), ss[0], _on(out, dev, "o"), B, H, Dk, Dv, code, stream)
         if rc:
             _check("gdn2_linear_decode_step", rc)
         return out
@@ -612,6 +619,7 @@ class DecayLinearAttention(torch.autograd.Function):
         return o, ST
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, do, dST):
         q, k, v, log_decay, S0, cu = ctx.saved_tensors
         if do is None and dST is None:
@@ -646,6 +654,8 @@ def rope_axes(sections, device="cuda") -> torch.Tensor:
 
 def _rows_of(t, name, B, T, H, D):
     """Pointer and token stride of [B, T, H, D] whose heads are contiguous and whose tokens are evenly spaced."""
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
     sb, st, sh, sd = t.stride()
     if sd != 1 or (sh != D and H > 1) or (B > 1 and T > 1 and sb != T * st):
         raise ValueError("%s: a token's heads must be contiguous and the tokens evenly spaced" % name)
@@ -654,18 +664,19 @@ def _rows_of(t, name, B, T, H, D):
 
 def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved):
     """Checks of the arguments the forward and the backward share: (sizes, leading and positional C arguments)."""
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+    qs, ks, ps = q.shape, k.shape, positions.shape
+    if len(qs) != 4 or len(ks) != 4 or qs[0] != ks[0] or qs[1] != ks[1] or qs[3] != ks[3]:
         raise ValueError("q and k must be [B, T, Hq, D] and [B, T, Hk, D]")
-    B, T, Hq, D = q.shape
-    Hk = k.shape[2]
-    dev, dt = q.device, q.dtype
-    if k.dtype != dt or k.device != dev:
+    B, T, Hq, D = qs
+    Hk = ks[2]
+    dev, dt = q.get_device(), q.dtype
+    if k.dtype != dt or k.get_device() != dev:
         raise ValueError("q and k must be of one dtype and on one device")
     if positions.dtype not in (torch.int32, torch.int64):
         raise TypeError("positions must be int32 or int64")
-    if positions.dim() not in (2, 3) or positions.shape[-2:] != (B, T):
+    if len(ps) not in (2, 3) or ps[-2] != B or ps[-1] != T:
         raise ValueError("positions must be [B, T] or [axes, B, T] = [..., %d, %d]" % (B, T))
-    num_axes = positions.shape[0] if positions.dim() == 3 else 1
+    num_axes = ps[0] if len(ps) == 3 else 1
     if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be float32 [pairs]")
     P = inv_freq.shape[0]
@@ -675,12 +686,12 @@ def _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
     if not norm and (q_weight is not None or k_weight is not None):
         raise ValueError("a weight needs a norm: give eps")
     f32 = torch.float32
-    qp, qs = _rows_of(q, "q", B, T, Hq, D)
-    kp, ks = _rows_of(k, "k", B, T, Hk, D)
+    q_ptr, q_step = _rows_of(q, "q", B, T, Hq, D)
+    k_ptr, k_step = _rows_of(k, "k", B, T, Hk, D)
     tail = (_on(positions, dev, "positions"), positions.element_size(), num_axes, _on(inv_freq, dev, "inv_freq"),
             _opt(axes, dev, "axes", torch.int32, (P,)), P, 1 if interleaved else 0, 1 if norm else 0, eps if norm else 0.0,
             _opt(q_weight, dev, "q_weight", f32, (D,)), _opt(k_weight, dev, "k_weight", f32, (D,)))
-    return (B, T, Hq, Hk, D, _dt(q)), (qp, kp, qs, ks), tail
+    return (B, T, Hq, Hk, D, _dt(q)), (q_ptr, k_ptr, q_step, k_step), tail
 
 
 def gdn2_qk_norm_rope_fwd(q, k, positions, inv_freq, axes=None, q_weight=None, k_weight=None, eps: Optional[float] = 1e-6,
@@ -696,8 +707,9 @@ def gdn2_qk_norm_rope_fwd(q, k, positions, inv_freq, axes=None, q_weight=None, k
         sizes, lead, tail = _rope(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
         qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
         ko = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
-        rc = lib().gdn2_qk_norm_rope_fwd(*lead, *tail, _opt(qo, dev, "q_out", q.dtype, q.shape),
-                                         _opt(ko, dev, "k_out", q.dtype, k.shape), *sizes, stream)
+        qo_ptr = qo.data_ptr() if q_out is None else _opt(qo, dev, "q_out", q.dtype, q.shape)
+        ko_ptr = ko.data_ptr() if k_out is None else _opt(ko, dev, "k_out", q.dtype, k.shape)
+        rc = lib().gdn2_qk_norm_rope_fwd(*lead, *tail, qo_ptr, ko_ptr, *sizes, stream)
         if rc:
             _check("gdn2_qk_norm_rope_fwd", rc)
         return qo, ko
@@ -741,6 +753,7 @@ class QkNormRope(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, positions, inv_freq, axes, q_weight, k_weight = ctx.saved_tensors
         g = gdn2_qk_norm_rope_bwd(q, k, dq_out.contiguous(), dk_out.contiguous(), positions, inv_freq, axes, q_weight,

@@ -235,6 +235,47 @@ def test_inconsistent_lengths_are_reported(dtype):
     assert binding.gdn2_device_status() == binding.GDN2_OK
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_no_room_for_tokens_hands_the_states_on_and_reports(dtype):
+    x, d, cu = packed_case([5, 0], 2, 64, 64, dtype, 24)
+    args = (d["q"], d["k"], d["v"], d["g"])
+    empty = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for lengths, status in ((empty, binding.GDN2_OK), (cu, binding.GDN2_ERR_INVALID)):
+        o, ST = binding.gdn2_linear_varlen_fwd(*args, lengths, 0, d["S0"], o=torch.full_like(d["v"], 7.0))
+        g = binding.gdn2_linear_varlen_bwd(*args, d["do"], lengths, 0, d["S0"], d["dST"])
+        assert binding.gdn2_device_status() == status
+        assert torch.equal(ST, d["S0"]) and torch.equal(g["dS0"], d["dST"]) and bool((o == 7.0).all())
+
+
+# a state that grows: a head's 128-token power stays finite in 32 bits (e^0.3 per token: e^38)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [100, 128])
+def test_growing_states(dtype, T):
+    x, d = make((1, T), 1, 3, 64, 64, dtype, 25, [0.3, 0.05, 0.0])
+    check_dense(x, d, dtype)
+
+
+# more segments than a block has items, and a bound on the length far above the lengths
+def test_many_segments_and_a_loose_bound():
+    lengths = [9000, 0, 333, 129]
+    x, d, cu = packed_case(lengths, 1, 64, 64, "bf16", 26)
+    args = (d["q"], d["k"], d["v"], d["g"])
+    o, ST = binding.gdn2_linear_varlen_fwd(*args, cu, 60000, d["S0"])
+    g = binding.gdn2_linear_varlen_bwd(*args, d["do"], cu, 60000, d["S0"], d["dST"])
+    assert binding.gdn2_device_status() == binding.GDN2_OK
+    f = {n: to_f64(t) for n, t in x.items()}
+    for i in range(len(lengths)):
+        at = slice(sum(lengths[:i]), sum(lengths[:i + 1]))
+        part = {m: f[m][at][None] for m in ("q", "k", "v", "do")}
+        o_ref, ST_ref = lin.fwd(part["q"], part["k"], part["v"], f["g"], f["S0"][i:i + 1])
+        ref = lin.bwd(part["q"], part["k"], part["v"], f["g"], part["do"], f["S0"][i:i + 1], f["dST"][i:i + 1])
+        check_tokens(to_f64(o)[at][None], o_ref, "bf16", ("o", i))
+        check_states(to_f64(ST)[i:i + 1], ST_ref, "bf16", ("ST", i))
+        for m in ("dq", "dk", "dv"):
+            check_tokens(to_f64(g[m])[at][None], ref[m], "bf16", (m, i))
+        check_states(to_f64(g["dS0"])[i:i + 1], ref["dS0"], "bf16", ("dS0", i))
+
+
 # ------------------------------------------------------------------ the single-token step
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -340,6 +381,15 @@ def test_autograd(dtype, packed):
     o, ST = binding.decay_linear_attention(*leaves[:3], d["g"], leaves[3], *((cu, max(lengths)) if packed else ()))
     (dk,) = torch.autograd.grad(ST.sum(), [leaves[1]])
     assert bool(dk.isfinite().all()) and bool(dk.any())
+
+
+def test_second_derivatives_are_refused():
+    x, d = make((1, 40), 1, 2, 64, 64, "f32", 52)
+    q = d["q"].requires_grad_()
+    o, _ = binding.decay_linear_attention(q, d["k"], d["v"], d["g"])
+    (dq,) = torch.autograd.grad((o * o).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dq.sum().backward()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

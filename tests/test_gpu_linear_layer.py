@@ -188,3 +188,35 @@ def test_prompts_then_steps(dtype):
         got = torch.cat([y[a:a + lengths[r]], torch.stack([o[i] for o in out])])
         assert rel_l2(got.double().cpu().numpy(), y_ref.numpy()) <= TOL_Y[dtype]
         assert rel_l2(pool[slots[i]].double().cpu().numpy(), S_ref.numpy()) <= TOL_Y[dtype]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_training_step_in_a_graph(dtype):
+    """Forward and backward captured after a warm-up on the capturing stream, replayed on new inputs."""
+    layer = layer_of(dtype, 96, 2, 64, 32)
+    x = torch.randn(2, 150, 96, device="cuda").to(DT[dtype])
+    pos = torch.arange(150, dtype=torch.int32, device="cuda").expand(2, 150).contiguous()
+    S0 = torch.randn(2, 2, 64, 32, device="cuda")
+    dy = torch.randn(2, 150, 96, device="cuda").to(DT[dtype])
+
+    def step():
+        y, ST = layer(x, S0, pos)
+        return [y.detach(), ST.detach(), *torch.autograd.grad((y * dy).sum() + ST.sum(), list(layer.parameters()))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn(2, 150, 96))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
