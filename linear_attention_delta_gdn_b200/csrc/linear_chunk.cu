@@ -9,6 +9,14 @@
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
+// What bounds it: a chunk takes a block 1.86 us (3500 cycles at 1.9 GHz), of which its products are 1670 of the tensor
+// pipe alone (64 cycles a K step at N 128, 48 at N 64 from shared memory, 32 from TMEM) and their operands 1500 of shared
+// memory's; no role is busy all the time and none waits for one other alone, so it is the round trips between the roles.
+// Measured: 73 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 57% of the copy rate; 30% of the tensor pipe's cycles,
+// 128 blocks), 280 us with the backward, 374 us for 65536 tokens of 16 heads from a stored state (two launches).
+// Tried and slower: Zh and Zl made before D is waited for (registers), Zh and Zl in two buffers with the outputs stored
+// from registers (76 us), P shared between two warpgroups (90 us), the product loops unrolled (no gain).
+//
 // Roundings. P and the copy of R round to bf16 (2^-8 each at most): they feed out, which is bf16 itself. The state is
 // a 32-bit result, so g_j z_j goes into D as two bf16 terms, hi and the rest: 2^-18, where one term would leave 2^-9
 // in a state that every later token reads. Sums are 32-bit.

@@ -12,6 +12,10 @@
 // The products run on tensor cores with every 32-bit operand split into two tf32 terms, x = big + small (11 + 11
 // significant bits): big big + big small + small big leaves out terms below 2^-22, about what 32-bit rounding of a
 // long sum costs, where plain tf32 operands would leave 2^-11. Sums are 32-bit.
+//
+// This is the path for checks of a model's numerics; its work is the products' (three mma.sync for one, and the splitting
+// of each operand, 47% of the issue slots in chunk_out_kernel), its time that of the launches where there are few tokens:
+// training on 2 x 1001 tokens, 4 heads of 64, takes 59 us in six launches, 2 x 13 in the outputs of one pass.
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"

@@ -2,6 +2,8 @@
 //     S <- a_h S + k v^T,   o = S^T q,   on the states of a pool that the requests' slots name.
 //
 // The state is read and written once, 8 Dk Dv bytes a request and head, against 5 Dk Dv operations: the memory bound.
+// A block a state and all its rows in flight: 256 requests of 16 heads of 128 x 128 take 83 us, 6.4 TB/s (97% of the copy
+// rate); one request, its states spread over 64 blocks of 32 columns, 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

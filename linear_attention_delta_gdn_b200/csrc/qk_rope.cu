@@ -11,6 +11,9 @@
 // makes its cosines and sines once, each lane keeps those of its channels in registers, and the token's rows pass by,
 // several in flight as they lie in memory, 16 bytes a lane at each of a pair's two places. What an angle needs 64 bits
 // for does not depend on the token and is made once a block. Few tokens: several warps share a token's heads.
+// Measured: 4 x 4096 tokens of 16 + 16 heads of 128 take 54 us, 4.9 TB/s (76% of the copy rate); 2 x 3999 tokens of 16 + 4
+// heads with the backward and both weights' gradients 58 us (the forward 24, the backward 35: loads of few rows a token
+// to wait for); 64 tokens of one serving step 3.6 us, the latency of the loads.
 // Far positions: the angle is a whole-number product modulo one turn, so a position of millions (or of 2^40) keeps the
 // error of a small one (a 32-bit product is off by 0.06 at a million).
 #include <cuda_bf16.h>
