@@ -9,13 +9,15 @@
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
-// What bounds it: a chunk takes a block 1.86 us (3500 cycles at 1.9 GHz), of which its products are 1670 of the tensor
-// pipe alone (64 cycles a K step at N 128, 48 at N 64 from shared memory, 32 from TMEM) and their operands 1500 of shared
-// memory's; no role is busy all the time and none waits for one other alone, so it is the round trips between the roles.
-// Measured: 73 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 57% of the copy rate; 30% of the tensor pipe's cycles,
+// What bounds it: a chunk takes a block 1.8 us (3400 cycles), for rows of 64 as for 128 and for one block as for 128 of
+// them, so it is the round trips between the roles. Its products are 1670 cycles of the tensor pipe alone (64 a K step at
+// N 128, 48 at N 64 from shared memory, 32 from TMEM); the pairs' warpgroup works 2800 (P 1300 and outputs 1300), the
+// values' 2200, the state's 1200; a chunk's tiles take 2400 from request to arrival, and X, held from its A to its O1 a
+// chunk later, has two stages. Measured: 73 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 57% of the copy rate; 30% of the tensor pipe's cycles,
 // 128 blocks), 280 us with the backward, 374 us for 65536 tokens of 16 heads from a stored state (two launches).
-// Tried and slower: Zh and Zl made before D is waited for (registers), Zh and Zl in two buffers with the outputs stored
-// from registers (76 us), P shared between two warpgroups (90 us), the product loops unrolled (no gain).
+// Tried and not faster: Zh and Zl made before D is waited for (registers), Zh and Zl in two buffers with the outputs stored
+// from registers (76 us), three buffers of Z through TMA with rolled loops (74 us), X in three stages (79 us), P shared
+// between two warpgroups (90 us), A ahead of D (78 us), the product loops unrolled (73 us).
 //
 // Roundings. P and the copy of R round to bf16 (2^-8 each at most): they feed out, which is bf16 itself. The state is
 // a 32-bit result, so g_j z_j goes into D as two bf16 terms, hi and the rest: 2^-18, where one term would leave 2^-9
@@ -208,8 +210,11 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
     uint32_t ny = 0;   // stages asked for so far, over all items
     bool ok = true;
     // Two stages of X and Y cover the time of a read from L2, not that of one from memory: what comes AHEAD chunks later
-    // is brought into L2 meanwhile, X and Y by one of a head's slices each.
+    // is brought into L2 meanwhile, X and Y by one of a head's slices each. With two stages a chunk's own loads are late
+    // already and go first (4 x 4096 tokens, 16 heads of 128, from memory: 72.9 against 74.4 us, 78.2 without prefetches);
+    // with four the prefetches do (training on six packed sequences, 12 heads of 64: 149 against 160 us).
     constexpr int AHEAD = 3;
+    constexpr bool LOADS_FIRST = K::STAGES == 2;
     auto into_l2 = [&](const Item& t, int i) {
         const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
 #pragma unroll 1
@@ -224,7 +229,7 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
         for (int i = 1; i < AHEAD && i < t.count(); ++i) into_l2(t, i);
         for (int i = 0; i < t.count(); ++i) {
             const uint32_t s = ny % K::STAGES, ph = ((ny / K::STAGES) & 1) ^ 1;
-            if (i + AHEAD < t.count()) into_l2(t, i + AHEAD);
+            if (!LOADS_FIRST && i + AHEAD < t.count()) into_l2(t, i + AHEAD);
             const int row = (int)(t.row0 + (long long)t.chunk(i) * CT);
             if (!(ok = wait(&b.d_done[s], ph))) break;
             mbar_arrive_expect_tx(&b.full[s], K::YB);
@@ -239,6 +244,7 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
                 for (int c = 0; c < DRP / 64; ++c)
                     tma_load_3d(sm + s * K::XB + c * CT * 128, &t.p->x, 64 * c, t.h, row, &b.full[s]);
             }
+            if (LOADS_FIRST && i + AHEAD < t.count()) into_l2(t, i + AHEAD);
         }
     }
     if (ok) return;   // every tile was waited for by those who read it
