@@ -13,8 +13,9 @@
 // them: the round trips between the roles. Its products are 1670 cycles of the tensor pipe alone (64 a K step at
 // N 128, 48 at N 64 from shared memory, 32 from TMEM); the pairs' warpgroup works 2800 (P 1300 and outputs 1300), the
 // values' 2200, the state's 1200; a chunk's tiles take 2400 from request to arrival, and X, held from its A to its O1 a
-// chunk later, has two stages. Measured: 73 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 58% of the copy rate; 30% of the tensor pipe's cycles,
-// 128 blocks), 279 us with the backward, 380 us for 65536 tokens of 16 heads from a stored state (two launches).
+// chunk later, has two stages. Measured: 72 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 58% of the copy rate; 30% of
+// the tensor pipe's cycles, 128 blocks), 279 us with the backward, 380 us for 65536 tokens of 16 heads from a stored
+// state (two launches).
 // Tried and not faster: Zh and Zl made before D is waited for (registers), Zh and Zl in two buffers with the outputs stored
 // from registers (76 us), three buffers of Z through TMA with rolled loops (74 us), X in three stages (79 us), P shared
 // between two warpgroups (90 us), A ahead of D (78 us), the product loops unrolled (73 us).
