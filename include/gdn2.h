@@ -374,10 +374,11 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
  * ST. Rows behind the last sequence are not written. A sequence longer than
  * Tmax is cut at Tmax, one outside [0, Ttot) is skipped, and
  * gdn2_device_status then returns GDN2_ERR_INVALID with the detail
- * "cu_seqlens".
+ * "cu_seqlens". Any Tmax from the longest length on gives the same results
+ * (2^31 - 1: no bound); one above Ttot counts as Ttot.
  * Workspace: gdn2_linear_workspace_size(GDN2_OP_FWD or GDN2_OP_BWD, ...) bytes,
- * 256-byte aligned, with N = B and T for a dense call, N and Tmax for a packed
- * one; nothing in it outlives the call. 0 for another op or an invalid problem.
+ * 256-byte aligned, with N = B and T for a dense call, N and the smaller of Tmax
+ * and Ttot for a packed one; nothing in it outlives the call. 0 for another op or an invalid problem.
  */
 size_t gdn2_linear_workspace_size(gdn2_op op, int N, int T, int H, int Dk, int Dv, gdn2_dtype dt);
 gdn2_status gdn2_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,

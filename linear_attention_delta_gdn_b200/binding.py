@@ -487,7 +487,7 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
     if packed:
         if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 2:
             raise ValueError("cu_seqlens must be int32 [N + 1]")
-        N, T = cu.numel() - 1, int(Tmax)
+        N, T = cu.numel() - 1, min(int(Tmax), lead[0])   # no sequence is longer than the tensor
     else:
         N, T = lead
     bwd = dout is not None

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "linear_cut.h"
 
 namespace gdn2 {
 namespace linear {

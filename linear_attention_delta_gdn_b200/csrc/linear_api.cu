@@ -73,10 +73,12 @@ size_t workspace(const linear::Seqs& s, gdn2_dtype dt, bool bwd) {
     return align256(dt == GDN2_BF16 ? linear_chunk_workspace(s, bwd) : linear32_workspace(s, bwd));
 }
 
-gdn2_status run(const linear::Seqs& seq, const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
+gdn2_status run(linear::Seqs seq, const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
                 const void* dout, const float* dST, void* o, float* ST, void* dq, void* dk, void* dv, float* dS0, bool bwd,
                 gdn2_dtype dt, void* ws, size_t ws_bytes, void* stream, const char* fn) {
     NvtxRange nvtx(fn);
+    // no sequence of a packed call is longer than its tensor, however loose the bound: plans, grids and workspace go by that
+    if (seq.cu && seq.Ttot >= 0 && seq.T > seq.Ttot) seq.T = (int)seq.Ttot;
     gdn2_status st = check_dims(seq, dt);
     if (st != GDN2_OK) return st;
     REQUIRE_WORD_PTR(log_decay);

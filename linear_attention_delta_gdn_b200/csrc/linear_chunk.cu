@@ -46,12 +46,13 @@
 namespace gdn2 {
 namespace {
 
+using linear::Cut;
 using linear::Seqs;
 using namespace tc;
 
 __device__ unsigned int g_linear_error;
 
-constexpr int CT = 128;         // tokens of a chunk
+constexpr int CT = linear::CHUNK;   // tokens of a chunk
 constexpr int SL = 64;          // columns of a slice
 constexpr int NT = 512;         // threads of a block
 constexpr int MAX_PASS = 3;
@@ -100,11 +101,11 @@ __device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
     t->seg = x / N;
     t->p = &p.pass[t->pass];
     t->len = linear::seq_span(p.seq, t->n, &t->row0, &g_linear_error);
-    t->nc = (t->len + CT - 1) / CT;
+    t->nc = linear::pieces(t->len, CT);
     t->c0 = (int)min((long long)t->nc, (long long)t->seg * p.cps);
     t->c1 = min(t->nc, t->c0 + p.cps);
     if (STATES) {   // nothing comes behind the last segment (in front of the first one, backwards)
-        const int last = (t->nc + p.cps - 1) / p.cps - 1;
+        const int last = linear::pieces(t->nc, p.cps) - 1;
         if (t->p->rev ? t->seg == 0 : t->seg >= last) t->c1 = t->c0;
     }
     t->l2 = linear::log2_decay(p.log_decay, t->h);
@@ -113,7 +114,7 @@ __device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
 // ceil(len / S) of them never reach (row0 + len) / S + n + 1, where the next sequence's begin.
 template <int DRP>
 __device__ __forceinline__ float* segment_state(const Params& p, const Item& t, int seg) {
-    const long long slot = t.row0 / (p.cps * CT) + t.n + seg;
+    const long long slot = t.row0 / ((long long)p.cps * CT) + t.n + seg;
     return t.p->seg + ((slot * p.seq.H + t.h) * p.slices + t.slice) * (long long)(SL * DRP);
 }
 // The block's first item is found once, before the roles start (its loads and the first reads of the parameters take as
@@ -282,7 +283,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
     };
     auto settle = [&](Cursor& c) {   // to the cursor's chunk, into the next items if need be; false behind the last
         while (c.i >= c.count) {
-            if (c.count >= 0) c.x += gridDim.x;
+            c.x += gridDim.x;
             if (c.x >= p.items) return false;
             const Item t = item_of<STATES>(p, c.x);
             c.i = 0;
@@ -308,8 +309,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
         ++c.i;
         ++c.n;
     };
-    Cursor cur{(int)blockIdx.x, 0, -1, false, false, 0}, ahead = cur;
-    cur.i = ahead.i = 0;
+    Cursor cur{(int)blockIdx.x - (int)gridDim.x, 0, 0, false, false, 0}, ahead = cur;   // in front of the first item
     if (!STATES && settle(ahead)) issue_pairs(ahead);
     while (ok && settle(cur)) {
         const uint32_t n = cur.n, s = n % K::STAGES, ph = (n / K::STAGES) & 1, d = n & 1, one = n & 1;
@@ -601,7 +601,8 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
     if (STATES || !real) return;
     const Pass& q = *t.p;
     const size_t head = (size_t)t.n * p.seq.H + t.h;
-    const int seg_tokens = p.cps * CT, nseg = (t.nc + p.cps - 1) / p.cps;
+    const long long seg_tokens = (long long)p.cps * CT;
+    const int nseg = linear::pieces(t.nc, p.cps);
     // the start state under its decay, then the segments' states between it and here, each under its own
     const int from = q.rev ? t.seg + 1 : 0, to = q.rev ? nseg : t.seg;
 #pragma unroll 1
@@ -610,7 +611,7 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
         if (first && (!q.start || r >= p.dr)) continue;
         // tokens between where that state stands and this segment
         const long long away = !first ? (long long)(q.rev ? o - t.seg - 1 : t.seg - 1 - o) * seg_tokens
-                               : q.rev ? max(0ll, t.len - (t.seg + 1ll) * seg_tokens) : (long long)t.seg * seg_tokens;
+                               : q.rev ? max(0ll, t.len - (t.seg + 1) * seg_tokens) : t.seg * seg_tokens;
         const float f = linear::decay_pow(t.l2, (int)away);
         if (first && !q.start_transposed) {
             const float* src = q.start + (head * p.dr + r) * p.dz + t.slice * SL;
@@ -652,7 +653,7 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
     bool ok = true;
     for (int x = blockIdx.x; ok && x < p.items; x += gridDim.x) {
         const Item t = item_of<STATES>(p, x);
-        const bool last_seg = t.p->rev ? t.seg == 0 : t.seg == max(0, (t.nc + p.cps - 1) / p.cps - 1);
+        const bool last_seg = t.p->rev ? t.seg == 0 : t.seg == max(0, linear::pieces(t.nc, p.cps) - 1);
         const bool writes_end = !STATES && t.p->end && last_seg;
         if (t.count() == 0 && !writes_end) continue;
         start_state<DRP, STATES>(p, t, r, real, S);
@@ -788,49 +789,9 @@ int sm_count() {
     return n;
 }
 
-// How a sequence's chunks are cut: segments of cps chunks, nseg of them at most, `slots` states for them all (and head
-// and slice).
-struct Cut {
-    int nseg, cps;
-    long long slots;
-};
-// Items of a call that is cut at all, at most: its workspace is sized by them (a packed call's lengths are not known then).
-long long most_items(long long heads) { return 2 * heads + 4 * sm_count(); }
-bool may_cut(const Seqs& s, long long heads) { return s.T > CT && heads < 4 * sm_count(); }
-// Time in chunks of one block (1.9 us): the fullest block's chunks and 4 more for each of its items' start and end, in
-// more than one segment also 1.5 for each segment that an item's start is summed from, and the launch before, whose chunks
-// cost half as much (a sequence's last segment has none there), with 3 for the launch itself. Sequences of one length go in
-// waves. Of packed ones only the sum of their lengths is known here: the fullest block is taken to have the mean and half
-// an item more, and an item without chunks costs 1. One sequence of 65536 tokens, 16 heads of 128: 951 us uncut, 675 / 465 /
-// 381 us in 2 / 3 / 4 segments (one wave), 403 us in 9 (two waves), 564 us in 5 (two waves, the second nearly empty). Eight
-// packed sequences of 12557 tokens in all, 8 heads of 64 x 128: 91 us uncut, 85 us in 2 or 3 segments, 105 us in 6.
-Cut choose_cut(const Seqs& s, long long heads) {
-    const int nc = (s.T + CT - 1) / CT, nsm = sm_count();
-    Cut best{1, std::max(nc, 1), 0};
-    if (!may_cut(s, heads)) return best;
-    const double total = (s.Ttot / (double)CT + 0.5 * s.N) * ((double)heads / s.N);   // packed chunks, over all heads
-    double best_time = 1e30;
-    for (int r = 1; r <= 64 && r <= nc; ++r) {
-        const int cps = (nc + r - 1) / r, nseg = (nc + cps - 1) / cps;
-        const long long slots = s.Ttot / (cps * CT) + s.N + 1;
-        if (nseg > 1 && slots * (heads / s.N) > most_items(heads)) break;
-        // a launch's time from the cost of a chunk and of an item, its segments a sequence, and of packed sequences its
-        // chunks and its items with chunks
-        auto time = [&](double chunk, double item, int segs, double chunks, double items) {
-            const double one = chunk * cps + item;
-            if (!s.cu) return (double)((heads * segs + nsm - 1) / nsm) * one;
-            return std::max(one, (chunk * chunks + 4 * items + std::max(0.0, (double)heads * nseg - items)) / nsm + 0.5 * one);
-        };
-        const double items = 0.5 * heads + total / cps;
-        double t = time(1.0, 4 + 1.5 * (nseg - 1), nseg, total, items);
-        if (nseg > 1) t += time(0.5, 4, nseg - 1, std::max(0.0, total - 0.5 * heads * cps), std::max(0.0, items - heads)) + 3;
-        if (t < best_time) {
-            best_time = t;
-            best = Cut{nseg, cps, nseg > 1 ? slots : 0};
-        }
-    }
-    return best;
-}
+long long most_items(long long heads) { return linear::most_items(heads, sm_count()); }
+bool may_cut(const Seqs& s, long long heads) { return linear::may_cut(s.T, heads, sm_count()); }
+Cut choose_cut(const Seqs& s, long long heads) { return linear::choose_cut(s.N, s.T, s.Ttot, s.cu != nullptr, heads, sm_count()); }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int padded(int d) { return d > 64 ? 128 : 64; }

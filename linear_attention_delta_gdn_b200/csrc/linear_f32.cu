@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(256) join_states_kernel(Seqs s, int nc, const 
     long long begin;
     const int len = linear::seq_span(s, n, &begin, &g_linear32_error);
     const float l2 = linear::log2_decay(log_decay, h);
-    const int mine = (len + C32 - 1) / C32;
+    const int mine = linear::pieces(len, C32);
     float S = job.start ? job.start[(size_t)head * dd + e] : 0.f;
     float* st = job.states + (size_t)head * nc * dd + e;
     const float whole = linear::decay_pow(l2, C32), last = linear::decay_pow(l2, len - (mine - 1) * C32);
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const f
     });
 }
 
-int chunks_of(const Seqs& s) { return (s.T + C32 - 1) / C32; }
+int chunks_of(const Seqs& s) { return linear::pieces(s.T, C32); }
 
 template <int DK, int DV>
 cudaError_t states(const LinearArgs& a, int nc, const StateJobs& jobs, int n, cudaStream_t s) {

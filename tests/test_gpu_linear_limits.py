@@ -1,0 +1,38 @@
+"""Linear attention with a decay per head on the GPU at the limits of its arguments, against the fp64 oracle. Tolerances
+are those of test_gpu_linear.py, whose checks these tests use."""
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_delta_gdn_b200 import binding
+from linear_attention_delta_gdn_b200.inputs import to_f64
+from oracle import linear as lin
+from test_gpu_linear import built, check_states, check_tokens, packed_case  # noqa: F401 (built: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def check_packed(x, d, cu, lengths, Tmax, dtype):
+    args = (d["q"], d["k"], d["v"], d["g"])
+    o, ST = binding.gdn2_linear_varlen_fwd(*args, cu, Tmax, d["S0"])
+    g = binding.gdn2_linear_varlen_bwd(*args, d["do"], cu, Tmax, d["S0"], d["dST"])
+    assert binding.gdn2_device_status() == binding.GDN2_OK, binding.last_error()
+    f = {n: to_f64(t) for n, t in x.items()}
+    for i, n in enumerate(lengths):
+        at = slice(sum(lengths[:i]), sum(lengths[:i + 1]))
+        part = {m: f[m][at][None] for m in ("q", "k", "v", "do")}
+        o_ref, ST_ref = lin.fwd(part["q"], part["k"], part["v"], f["g"], f["S0"][i:i + 1])
+        ref = lin.bwd(part["q"], part["k"], part["v"], f["g"], part["do"], f["S0"][i:i + 1], f["dST"][i:i + 1])
+        check_tokens(to_f64(o)[at][None], o_ref, dtype, ("o", i))
+        check_states(to_f64(ST)[i:i + 1], ST_ref, dtype, ("ST", i))
+        for m in ("dq", "dk", "dv"):
+            check_tokens(to_f64(g[m])[at][None], ref[m], dtype, (m, i))
+        check_states(to_f64(g["dS0"])[i:i + 1], ref["dS0"], dtype, ("dS0", i))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Tmax", [2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1])
+@pytest.mark.parametrize("lengths", [[300, 0, 41], [2600, 1]])
+def test_a_bound_far_above_the_lengths(dtype, Tmax, lengths):
+    x, d, cu = packed_case(lengths, 2, 64, 32, dtype, 70)
+    check_packed(x, d, cu, lengths, Tmax, dtype)
