@@ -468,13 +468,16 @@ int gdn2_trace_read(char* names, size_t names_cap, int* launches, double* ms, in
  * kernel then records the event in device memory, lets its own copies in flight
  * land, skips the rest of its work and exits (the outputs of that call are not
  * valid, the CUDA context stays usable). This call synchronises `stream` (a
- * cudaStream_t, NULL for the default stream), returns GDN2_ERR_TIMEOUT if such
- * an event was recorded since the previous call (gdn2_last_error names the
- * kernel and the kind of wait) and clears the record; GDN2_ERR_CUDA if the
- * stream holds a CUDA error, and GDN2_ERR_INVALID if a packed-sequence call met
- * an inconsistent cu_seqlens (see gdn2_varlen_fwd), a decode step a bad slot
- * (gdn2_linear_decode_step) or a rotation a bad axis (gdn2_qk_norm_rope_fwd). The entry points above never
- * synchronise, so this is the call that checks a finished step after the fact.
+ * cudaStream_t, NULL for the default stream) and returns what was recorded since
+ * the previous call on the current device: GDN2_ERR_TIMEOUT for such an event,
+ * else GDN2_ERR_INVALID if an index check of the debug build failed, a
+ * packed-sequence call met an inconsistent cu_seqlens (see gdn2_varlen_fwd), a
+ * decode step a bad slot (gdn2_linear_decode_step) or a rotation a bad axis
+ * (gdn2_qk_norm_rope_fwd). The record is cleared, and gdn2_last_error holds all of
+ * it: where several things happened each is named, waits (with the kernel and the
+ * kind of wait) first. GDN2_ERR_CUDA if the stream holds a CUDA error. The entry
+ * points above never synchronise, so this is the call that checks a finished step
+ * after the fact.
  */
 gdn2_status gdn2_device_status(void* stream);
 

@@ -768,9 +768,9 @@ def qk_norm_rope(q, k, positions, inv_freq, axes=None, q_weight=None, k_weight=N
 
 
 def gdn2_device_status(device=None) -> int:
-    """Synchronise the current stream and return the device-side status of the tensor-core kernels
-    (0, or GDN2_ERR_TIMEOUT if a bounded wait inside them gave up since the previous call; the record is
-    cleared). The detail is in :func:`last_error`."""
+    """Synchronise the current stream and return the kernels' device-side status since the previous call: 0,
+    GDN2_ERR_TIMEOUT if a bounded wait gave up, or GDN2_ERR_INVALID if a kernel met arguments that are wrong (an
+    inconsistent cu_seqlens, a bad slot or axis). The record is cleared; :func:`last_error` names all of it."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     return int(lib().gdn2_device_status(_stream(dev)))
 

@@ -1318,7 +1318,7 @@ cudaError_t chunk_bwd_launch(const ChunkBwdArgs& a, cudaStream_t s) {
 
 cudaError_t chunk_bwd_take_errors(unsigned int* bits) {
     cudaError_t e = cudaMemcpyFromSymbol(bits, g_bwd_error, sizeof(unsigned int));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *bits == 0) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_bwd_error, &zero, sizeof(unsigned int));
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "device_records.h"
 #include "gdn2.h"
 
 namespace gdn2 {
@@ -52,7 +53,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // true when cond holds; otherwise it sets GDN2_DBG_BIT in the kernel's error word and is false, and the caller
 // skips the access it guards, so the kernel returns normally and gdn2_device_status reports the failure.
 // Nothing traps. In release builds every check is the constant true and costs nothing.
-constexpr unsigned int GDN2_DBG_BIT = 1u << 30;
 #ifdef GDN2_DEBUG
 #define GDN2_IN(word, cond) ((cond) ? true : (atomicOr(&(word), ::gdn2::GDN2_DBG_BIT), false))
 #else

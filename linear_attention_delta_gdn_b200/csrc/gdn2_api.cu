@@ -13,6 +13,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "device_records.h"
 #include "gdn2.h"
 #include "internal.h"
 #include "linear.cuh"
@@ -32,7 +33,7 @@ struct NvtxRange {
 
 namespace {
 
-thread_local char g_err[512];
+thread_local char g_err[1024];   // room for every record of gdn2_device_status at once
 
 gdn2_status fail(gdn2_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 gdn2_status fail(gdn2_status s, const char* fmt, ...) {
@@ -160,39 +161,20 @@ const char* gdn2_last_error(void) { return g_err; }
 gdn2_status gdn2_device_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_status(e, "gdn2_device_status (stream)");
-    unsigned int fwd = 0, bwd = 0;
-    if ((e = chunk_fwd_take_errors(&fwd)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (forward record)");
-    if ((e = chunk_bwd_take_errors(&bwd)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (backward record)");
-    unsigned int vl = 0;
-    if ((e = varlen_take_errors(&vl)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (varlen record)");
-    unsigned int lin = 0, lin32 = 0, step = 0, rope = 0;
-    if ((e = linear_chunk_take_errors(&lin)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
-    if ((e = linear32_take_errors(&lin32)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
-    if ((e = linear_step_take_errors(&step)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (step record)");
-    if ((e = qk_rope_take_errors(&rope)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (rotation record)");
-    if (vl)
-        return fail(GDN2_ERR_INVALID, "cu_seqlens: %s%s", (vl & 1u) ? "a sequence was longer than Tmax (cut) " : "",
-                    (vl & 2u) ? "a sequence lay outside [0, Ttot) or had a negative length (dropped)" : "");
-    lin |= lin32;
-    if (lin & (linear::ERR_LONG | linear::ERR_OUTSIDE))
-        return fail(GDN2_ERR_INVALID, "cu_seqlens: %s%s", (lin & linear::ERR_LONG) ? "a sequence was longer than Tmax (cut) " : "",
-                    (lin & linear::ERR_OUTSIDE) ? "a sequence lay outside [0, Ttot) or had a negative length (dropped)" : "");
-    if (lin & linear::ERR_WAIT) return fail(GDN2_ERR_TIMEOUT, "device wait gave up: linear_chunk_kernel");
-    if (step & linear::ERR_SLOT)
-        return fail(GDN2_ERR_INVALID, "slots: a row's slot lay outside the pool, or an earlier row had named it (row skipped)");
-    if (rope) return fail(GDN2_ERR_INVALID, "axes: a pair's axis lay outside [0, num_axes) (pair not turned)");
-    if ((fwd | bwd) & GDN2_DBG_BIT)
-        return fail(GDN2_ERR_INVALID,
-                    "index check failed (debug build; the accesses it guarded were skipped): chunk_fwd_kernel bits "
-                    "0x%x, chunk_bwd_kernel bits 0x%x",
-                    fwd, bwd);
-    if (fwd | bwd)
-        return fail(GDN2_ERR_TIMEOUT,
-                    "device wait gave up: chunk_fwd_kernel bits 0x%x, chunk_bwd_kernel bits 0x%x "
-                    "(1 MMA completion, 2 tile loads, 4 forward ready flag / gradient unit, 8 backward ready flag, "
-                    "16 launched with a block size the kernel is not built for)",
-                    fwd, bwd);
-    return GDN2_OK;
+    DeviceRecords r{};
+    unsigned int linear32 = 0;
+    if ((e = chunk_fwd_take_errors(&r.fwd)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (forward record)");
+    if ((e = chunk_bwd_take_errors(&r.bwd)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (backward record)");
+    if ((e = varlen_take_errors(&r.varlen)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (varlen record)");
+    if ((e = linear_chunk_take_errors(&r.linear)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
+    if ((e = linear32_take_errors(&linear32)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (linear record)");
+    if ((e = linear_step_take_errors(&r.step)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (step record)");
+    if ((e = qk_rope_take_errors(&r.rope)) != cudaSuccess) return cuda_status(e, "gdn2_device_status (rotation record)");
+    r.linear |= linear32;
+    char text[sizeof(g_err)];
+    const gdn2_status status = describe_records(r, text, sizeof(text));
+    if (status != GDN2_OK) set_last_error(text);
+    return status;
 }
 
 size_t gdn2_workspace_size(gdn2_op op, int B, int T, int H, int Dk, int Dv, int chunk, gdn2_dtype dt) {

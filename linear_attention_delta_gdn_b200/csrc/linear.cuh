@@ -29,12 +29,6 @@ struct Seqs {
     int H, Dk, Dv;
 };
 
-// Error word bits of the linear kernels, read by gdn2_device_status.
-constexpr unsigned int ERR_LONG = 1u;      // a sequence longer than Tmax (cut)
-constexpr unsigned int ERR_OUTSIDE = 2u;   // a sequence outside [0, Ttot) or of negative length (dropped)
-constexpr unsigned int ERR_SLOT = 4u;      // a decode slot outside the pool or named twice (skipped)
-constexpr unsigned int ERR_WAIT = 8u;      // a bounded wait gave up
-
 // First token row and length of sequence n; records an inconsistent cu_seqlens.
 __device__ __forceinline__ int seq_span(const Seqs& s, int n, long long* begin, unsigned int* err) {
     if (!s.cu) {

@@ -199,7 +199,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
         ok = wait(bar, phase);
-        if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
+        if (!ok) atomicOr(&g_linear_error, ERR_WAIT);
     }
     return __shfl_sync(0xffffffffu, ok, 0);
 }
@@ -250,7 +250,7 @@ __device__ void load_tiles(const Params& p, unsigned char* sm, Bars& b) {
         }
     }
     if (ok) return;   // every tile was waited for by those who read it
-    atomicOr(&g_linear_error, linear::ERR_WAIT);
+    atomicOr(&g_linear_error, ERR_WAIT);
     // let the copies in flight land before the block gives up its shared memory: each stage's last ones. A stage whose X
     // was not asked for any more keeps its barrier open; its Y has the time that wait takes.
     for (uint32_t k = 1; k <= (uint32_t)K::STAGES && k <= ny; ++k)
@@ -339,7 +339,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
             mma_bf16_ts(tm + K::T_O2, tm + K::T_A + d * CT + 8 * kk, zmn + MN * kk, idO, kk > 0);
         mma_commit(&b.o2_done[d]);
     }
-    if (!ok) atomicOr(&g_linear_error, linear::ERR_WAIT);
+    if (!ok) atomicOr(&g_linear_error, ERR_WAIT);
     // what was issued ends before TMEM is given back
     mma_commit(&b.drain);
     wait(&b.drain, 0);
@@ -914,7 +914,7 @@ cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
 
 cudaError_t linear_chunk_take_errors(unsigned int* bits) {
     cudaError_t e = cudaMemcpyFromSymbol(bits, g_linear_error, sizeof(unsigned int));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *bits == 0) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(unsigned int));
 }

@@ -352,7 +352,7 @@ cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
 
 cudaError_t linear32_take_errors(unsigned int* bits) {
     cudaError_t e = cudaMemcpyFromSymbol(bits, g_linear32_error, sizeof(unsigned int));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *bits == 0) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_linear32_error, &zero, sizeof(unsigned int));
 }

@@ -54,7 +54,7 @@ linear_step_kernel(const Tin* __restrict__ q, const Tin* __restrict__ k, const T
         mine = !__syncthreads_or(earlier);
     }
     if (!mine) {
-        if (tid == 0 && slot >= 0) atomicOr(&g_step_error, linear::ERR_SLOT);
+        if (tid == 0 && slot >= 0) atomicOr(&g_step_error, ERR_SLOT);
         for (int j = tid; j < CS; j += L::NT) out[j] = from_f32<Tin>(0.f);
         return;
     }
@@ -129,7 +129,7 @@ cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t s) {
 
 cudaError_t linear_step_take_errors(unsigned int* bits) {
     cudaError_t e = cudaMemcpyFromSymbol(bits, g_step_error, sizeof(unsigned int));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *bits == 0) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_step_error, &zero, sizeof(unsigned int));
 }

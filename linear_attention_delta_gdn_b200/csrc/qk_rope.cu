@@ -472,7 +472,7 @@ cudaError_t qk_rope_launch(const QkRopeArgs& a, float* ws, cudaStream_t s) {
 
 cudaError_t qk_rope_take_errors(unsigned int* bits) {
     cudaError_t e = cudaMemcpyFromSymbol(bits, g_rope_error, sizeof(unsigned int));
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || *bits == 0) return e;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(unsigned int));
 }

@@ -36,3 +36,17 @@ def check_packed(x, d, cu, lengths, Tmax, dtype):
 def test_a_bound_far_above_the_lengths(dtype, Tmax, lengths):
     x, d, cu = packed_case(lengths, 2, 64, 32, dtype, 70)
     check_packed(x, d, cu, lengths, Tmax, dtype)
+
+
+def test_every_record_is_named():
+    """A bad slot, a sequence cut at Tmax and a bad axis between two readings: each is in the detail."""
+    x, d, cu = packed_case([70, 30], 2, 64, 64, "bf16", 71)
+    binding.gdn2_device_status()
+    args = (d["q"], d["k"], d["v"], d["g"])
+    binding.gdn2_linear_decode_step(*(t[:2] for t in args[:3]), args[3], d["S0"].clone(), torch.tensor([1, 1], dtype=torch.int32).cuda())
+    binding.gdn2_linear_varlen_fwd(*args, cu, 64)
+    pos, f = torch.zeros(1, 100, dtype=torch.int32, device="cuda"), torch.ones(8, device="cuda")
+    binding.gdn2_qk_norm_rope_fwd(args[0][None], args[1][None], pos, f, torch.full((8,), 3, dtype=torch.int32, device="cuda"))
+    assert binding.gdn2_device_status() == binding.GDN2_ERR_INVALID
+    assert all(s in binding.last_error() for s in ("slots", "Tmax", "axes")), binding.last_error()
+    assert binding.gdn2_device_status() == binding.GDN2_OK
