@@ -1316,11 +1316,8 @@ cudaError_t chunk_bwd_launch(const ChunkBwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t chunk_bwd_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_bwd_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_bwd_error, &zero, sizeof(unsigned int));
+cudaError_t chunk_bwd_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_bwd_error);
 }
 
 }  // namespace gdn2

@@ -1359,11 +1359,8 @@ cudaError_t chunk_fwd_launch(const ChunkFwdArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t chunk_fwd_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_fwd_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_fwd_error, &zero, sizeof(unsigned int));
+cudaError_t chunk_fwd_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_fwd_error);
 }
 
 }  // namespace gdn2

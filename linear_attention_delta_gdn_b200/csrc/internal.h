@@ -141,10 +141,10 @@ class TraceScope {
 // their producer and consumer work as two ordinary launches instead of one cooperative launch.
 bool cooperative_disabled();
 bool test_skip_producers();   // host-side fault injection for the forward's two-launch form
-// Read and clear the device-side error words of the tensor-core kernels (bit set: a bounded wait gave up).
-cudaError_t chunk_fwd_take_errors(unsigned int* bits);
-cudaError_t chunk_bwd_take_errors(unsigned int* bits);
-cudaError_t varlen_take_errors(unsigned int* bits);   // bit 1: a sequence longer than Tmax; 2: outside [0, Ttot)
+// The kernels' error words on the current device; gdn2_device_status reads and clears them (device_records.h has the bits).
+cudaError_t chunk_fwd_error_word(unsigned int** word);
+cudaError_t chunk_bwd_error_word(unsigned int** word);
+cudaError_t varlen_error_word(unsigned int** word);   // bit 1: a sequence longer than Tmax; 2: outside [0, Ttot)
 
 // Sets the detail string returned by gdn2_last_error() on this host thread.
 void set_last_error(const char* msg);

@@ -72,12 +72,12 @@ struct LinearArgs {
 // fp32 (linear_f32.cu)
 size_t linear32_workspace(const linear::Seqs& s, bool backward);
 cudaError_t linear32_launch(const LinearArgs& a, bool backward, cudaStream_t s);
-cudaError_t linear32_take_errors(unsigned int* bits);
+cudaError_t linear32_error_word(unsigned int** word);
 
 // bf16 on tensor cores (linear_chunk.cu)
 size_t linear_chunk_workspace(const linear::Seqs& s, bool backward);
 cudaError_t linear_chunk_launch(const LinearArgs& a, bool backward, cudaStream_t s);
-cudaError_t linear_chunk_take_errors(unsigned int* bits);
+cudaError_t linear_chunk_error_word(unsigned int** word);
 
 struct LinearStepArgs {
     gdn2_dtype dt;
@@ -90,6 +90,6 @@ struct LinearStepArgs {
     int B, H, Dk, Dv;
 };
 cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t s);
-cudaError_t linear_step_take_errors(unsigned int* bits);
+cudaError_t linear_step_error_word(unsigned int** word);
 
 }  // namespace gdn2

@@ -912,11 +912,8 @@ cudaError_t linear_chunk_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
     return e != cudaSuccess ? e : run_group(a, one, cut, s);
 }
 
-cudaError_t linear_chunk_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_linear_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_linear_error, &zero, sizeof(unsigned int));
+cudaError_t linear_chunk_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear_error);
 }
 
 }  // namespace gdn2

@@ -350,11 +350,8 @@ cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {
     return run_dk(a, bwd, s);
 }
 
-cudaError_t linear32_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_linear32_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_linear32_error, &zero, sizeof(unsigned int));
+cudaError_t linear32_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_linear32_error);
 }
 
 }  // namespace gdn2

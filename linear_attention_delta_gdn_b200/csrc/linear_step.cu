@@ -127,11 +127,8 @@ cudaError_t linear_step_launch(const LinearStepArgs& a, cudaStream_t s) {
     return a.dt == GDN2_BF16 ? step_rows<__nv_bfloat16>(a, s) : step_rows<float>(a, s);
 }
 
-cudaError_t linear_step_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_step_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_step_error, &zero, sizeof(unsigned int));
+cudaError_t linear_step_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_step_error);
 }
 
 }  // namespace gdn2

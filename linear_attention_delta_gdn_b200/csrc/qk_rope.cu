@@ -470,11 +470,8 @@ cudaError_t qk_rope_launch(const QkRopeArgs& a, float* ws, cudaStream_t s) {
     return a.dt == GDN2_BF16 ? run_t<__nv_bfloat16>(a, ws, s) : run_t<float>(a, ws, s);
 }
 
-cudaError_t qk_rope_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_rope_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_rope_error, &zero, sizeof(unsigned int));
+cudaError_t qk_rope_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_rope_error);
 }
 
 }  // namespace gdn2

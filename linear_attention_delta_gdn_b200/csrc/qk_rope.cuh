@@ -27,6 +27,6 @@ struct QkRopeArgs {
 };
 constexpr int QK_ROPE_BLOCKS = 148 * 2;   // blocks of the backward at most: each leaves one weight's partial gradient
 cudaError_t qk_rope_launch(const QkRopeArgs& a, float* ws, cudaStream_t s);
-cudaError_t qk_rope_take_errors(unsigned int* bits);
+cudaError_t qk_rope_error_word(unsigned int** word);
 
 }  // namespace gdn2

@@ -163,11 +163,8 @@ gdn2_status cuda_fail(cudaError_t e, const char* where) {
 
 }  // namespace
 
-cudaError_t varlen_take_errors(unsigned int* bits) {
-    cudaError_t e = cudaMemcpyFromSymbol(bits, g_varlen_error, sizeof(unsigned int));
-    if (e != cudaSuccess || *bits == 0) return e;
-    const unsigned int zero = 0;
-    return cudaMemcpyToSymbol(g_varlen_error, &zero, sizeof(unsigned int));
+cudaError_t varlen_error_word(unsigned int** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_varlen_error);
 }
 
 }  // namespace gdn2
