@@ -771,8 +771,8 @@ def gdn2_device_status(device=None) -> int:
     """Synchronise the current stream and return the kernels' device-side status since the previous call: 0,
     GDN2_ERR_TIMEOUT if a bounded wait gave up, or GDN2_ERR_INVALID if a kernel met arguments that are wrong (an
     inconsistent cu_seqlens, a bad slot or axis). The record is cleared; :func:`last_error` names all of it."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    return int(lib().gdn2_device_status(_stream(dev)))
+    with torch.cuda.device(device):   # the record is the current device's
+        return int(lib().gdn2_device_status(torch.cuda.current_stream().cuda_stream))
 
 
 def last_error() -> str:

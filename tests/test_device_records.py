@@ -79,3 +79,35 @@ def test_all_at_once_fit_and_a_short_buffer_is_kept(describe):
     assert status == TIMEOUT and len(text) < 1023 and all(d in text for _, d in OTHERS.values())
     for cap in (0, 1, 2, 40):
         assert describe(words, cap) == (TIMEOUT, text[:max(cap - 1, 0)])
+
+
+def test_the_binding_asks_the_device_it_is_given(monkeypatch):
+    """The error words belong to a device: the call runs with the named one current, and on its stream."""
+    import torch
+    from linear_attention_delta_gdn_b200 import binding
+    current, asked = [0], []
+
+    class device:
+        def __init__(self, d):
+            self.d = current[0] if d is None else torch.device(d).index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.d
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Stream:
+        def __init__(self, d):
+            self.cuda_stream = 100 + (current[0] if d is None else torch.device(d).index)
+
+    class Lib:
+        def gdn2_device_status(self, stream):
+            asked.append((current[0], int(getattr(stream, "value", stream))))
+            return 0
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(d))
+    monkeypatch.setattr(binding, "lib", Lib)
+    assert binding.gdn2_device_status() == 0 and binding.gdn2_device_status("cuda:1") == 0
+    assert asked == [(0, 100), (1, 101)] and current == [0]
