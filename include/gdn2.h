@@ -376,11 +376,16 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
  * gdn2_device_status then returns GDN2_ERR_INVALID with the detail
  * "cu_seqlens". Any Tmax from the longest length on gives the same results
  * (2^31 - 1: no bound); one above Ttot counts as Ttot.
- * Workspace: gdn2_linear_workspace_size(GDN2_OP_FWD or GDN2_OP_BWD, ...) bytes,
- * 256-byte aligned, with N = B and T for a dense call, N and the smaller of Tmax
- * and Ttot for a packed one; nothing in it outlives the call. 0 for another op or an invalid problem.
+ * Workspace (256-byte aligned; nothing in it outlives the call):
+ * gdn2_linear_workspace_size(GDN2_OP_FWD or GDN2_OP_BWD, ...) bytes with N = B for
+ * a dense call, gdn2_linear_varlen_workspace_size(...) bytes for a packed one.
+ * Both return 0 for another op or an invalid problem. In float32 they grow with
+ * the tokens: a state for every 64 of a sequence, packed at most one for every 64
+ * rows and one more for each sequence, however loose Tmax is. In bf16 they do not.
  */
 size_t gdn2_linear_workspace_size(gdn2_op op, int N, int T, int H, int Dk, int Dv, gdn2_dtype dt);
+size_t gdn2_linear_varlen_workspace_size(gdn2_op op, int N, int Tmax, long long Ttot, int H, int Dk, int Dv,
+                                         gdn2_dtype dt);
 gdn2_status gdn2_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
                             void* o, float* ST, int B, int T, int H, int Dk, int Dv, gdn2_dtype dt, void* ws,
                             size_t ws_bytes, void* stream);

@@ -36,7 +36,7 @@ EXPORTS = ("gdn2_workspace_size", "gdn2_fwd", "gdn2_bwd", "gdn2_decode_step", "g
            "gdn2_trace_enable", "gdn2_trace_read", "gdn2_device_status", "gdn2_beta_workspace_size",
            "gdn2_beta_fwd", "gdn2_beta_bwd", "gdn2_varlen_workspace_size", "gdn2_varlen_fwd", "gdn2_varlen_bwd",
            "gdn2_fwd_map", "gdn2_bwd_map", "gdn2_state_affine", "gdn2_layer_gates_fwd", "gdn2_layer_gates_bwd",
-           "gdn2_linear_workspace_size", "gdn2_linear_fwd", "gdn2_linear_bwd", "gdn2_linear_varlen_fwd",
+           "gdn2_linear_workspace_size", "gdn2_linear_varlen_workspace_size", "gdn2_linear_fwd", "gdn2_linear_bwd", "gdn2_linear_varlen_fwd",
            "gdn2_linear_varlen_bwd", "gdn2_linear_decode_step", "gdn2_qk_norm_rope_workspace_size",
            "gdn2_qk_norm_rope_fwd", "gdn2_qk_norm_rope_bwd")
 GDN2_GATE_KDA, GDN2_GATE_GDN = 1, 2
@@ -102,6 +102,8 @@ def lib(path: Optional[str] = None) -> ctypes.CDLL:
     F = ctypes.c_float
     L.gdn2_linear_workspace_size.argtypes = [I] * 7
     L.gdn2_linear_workspace_size.restype = Z
+    L.gdn2_linear_varlen_workspace_size.argtypes = [I] * 3 + [LL] + [I] * 4
+    L.gdn2_linear_varlen_workspace_size.restype = Z
     L.gdn2_linear_fwd.argtypes = [P] * 7 + [I] * 6 + [P, Z, P]
     L.gdn2_linear_fwd.restype = I
     L.gdn2_linear_bwd.argtypes = [P] * 11 + [I] * 6 + [P, Z, P]
@@ -467,6 +469,10 @@ def gdn2_linear_workspace_size(op: int, N: int, T: int, H: int, Dk: int, Dv: int
     return int(lib().gdn2_linear_workspace_size(op, N, T, H, Dk, Dv, dt))
 
 
+def gdn2_linear_varlen_workspace_size(op: int, N: int, Tmax: int, Ttot: int, H: int, Dk: int, Dv: int, dt: int) -> int:
+    return int(lib().gdn2_linear_varlen_workspace_size(op, N, min(Tmax, Ttot), Ttot, H, Dk, Dv, dt))
+
+
 def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs, ends):
     """Shared by the four whole-sequence calls: checks, outputs, workspace, the call. Returns (outs, end state)."""
     packed = cu is not None
@@ -508,7 +514,9 @@ def _linear(fn, q, k, v, log_decay, S0, dout, dST, cu, Tmax, want_end, ws, outs,
         if end is None and want_end:
             end = q.new_empty(state, dtype=f32)
         L = lib()
-        need = L.gdn2_linear_workspace_size(GDN2_OP_BWD if bwd else GDN2_OP_FWD, N, T, H, Dk, Dv, code)
+        op = GDN2_OP_BWD if bwd else GDN2_OP_FWD
+        need = (L.gdn2_linear_varlen_workspace_size(op, N, T, lead[0], H, Dk, Dv, code) if packed else
+                L.gdn2_linear_workspace_size(op, N, T, H, Dk, Dv, code))
         if ws is None and need:
             ws = q.new_empty(need, dtype=torch.uint8)
         if packed:

@@ -69,8 +69,8 @@ struct LinearArgs {
     float *ST, *dS0;
     void* ws;
 };
-// fp32 (linear_f32.cu)
-size_t linear32_workspace(const linear::Seqs& s, bool backward);
+// fp32 (linear_f32.cu); packed: a varlen call with s.Ttot rows
+size_t linear32_workspace(const linear::Seqs& s, bool packed, bool backward);
 cudaError_t linear32_launch(const LinearArgs& a, bool backward, cudaStream_t s);
 cudaError_t linear32_error_word(unsigned int** word);
 

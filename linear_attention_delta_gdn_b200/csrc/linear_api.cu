@@ -69,16 +69,19 @@ gdn2_status check_dims(const linear::Seqs& s, gdn2_dtype dt) {
         if (!aligned((p), 4)) return fail(GDN2_ERR_INVALID, "%s must be 4-byte aligned", #p);  \
     } while (0)
 
-size_t workspace(const linear::Seqs& s, gdn2_dtype dt, bool bwd) {
-    return align256(dt == GDN2_BF16 ? linear_chunk_workspace(s, bwd) : linear32_workspace(s, bwd));
+size_t workspace(const linear::Seqs& s, gdn2_dtype dt, bool bwd, bool packed) {
+    return align256(dt == GDN2_BF16 ? linear_chunk_workspace(s, bwd) : linear32_workspace(s, packed, bwd));
+}
+// No sequence of a packed call is longer than its tensor, however loose the bound: plans, grids and workspace go by that.
+void tighten(linear::Seqs& s) {
+    if (s.Ttot >= 0 && s.T > s.Ttot) s.T = (int)s.Ttot;
 }
 
 gdn2_status run(linear::Seqs seq, const void* q, const void* k, const void* v, const float* log_decay, const float* S0,
                 const void* dout, const float* dST, void* o, float* ST, void* dq, void* dk, void* dv, float* dS0, bool bwd,
                 gdn2_dtype dt, void* ws, size_t ws_bytes, void* stream, const char* fn) {
     NvtxRange nvtx(fn);
-    // no sequence of a packed call is longer than its tensor, however loose the bound: plans, grids and workspace go by that
-    if (seq.cu && seq.Ttot >= 0 && seq.T > seq.Ttot) seq.T = (int)seq.Ttot;
+    if (seq.cu) tighten(seq);
     gdn2_status st = check_dims(seq, dt);
     if (st != GDN2_OK) return st;
     REQUIRE_WORD_PTR(log_decay);
@@ -93,7 +96,7 @@ gdn2_status run(linear::Seqs seq, const void* q, const void* k, const void* v, c
         } else {
             REQUIRE_PTR(o);
         }
-        const size_t need = workspace(seq, dt, bwd);
+        const size_t need = workspace(seq, dt, bwd, seq.cu != nullptr);
         if (need && (!ws || ws_bytes < need))
             return fail(GDN2_ERR_WORKSPACE, "%s needs %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
         if (need && !aligned(ws, 256)) return fail(GDN2_ERR_INVALID, "ws must be 256-byte aligned");
@@ -122,7 +125,15 @@ size_t gdn2_linear_workspace_size(gdn2_op op, int N, int T, int H, int Dk, int D
     if (op != GDN2_OP_FWD && op != GDN2_OP_BWD) return 0;
     const linear::Seqs s{nullptr, N, T, 0, H, Dk, Dv};
     if (check_dims(s, dt) != GDN2_OK) return 0;
-    return workspace(s, dt, op == GDN2_OP_BWD);
+    return workspace(s, dt, op == GDN2_OP_BWD, false);
+}
+
+size_t gdn2_linear_varlen_workspace_size(gdn2_op op, int N, int Tmax, long long Ttot, int H, int Dk, int Dv, gdn2_dtype dt) {
+    if (op != GDN2_OP_FWD && op != GDN2_OP_BWD) return 0;
+    linear::Seqs s{nullptr, N, Tmax, Ttot, H, Dk, Dv};
+    tighten(s);
+    if (check_dims(s, dt) != GDN2_OK) return 0;
+    return workspace(s, dt, op == GDN2_OP_BWD, true);
 }
 
 gdn2_status gdn2_linear_fwd(const void* q, const void* k, const void* v, const float* log_decay, const float* S0, void* o,

@@ -118,27 +118,37 @@ __device__ __forceinline__ void load_state(float* dst, const float* src) {
     constexpr int PER = D / 4;
     for (int x = threadIdx.x; x < R * PER; x += NT32) tc::cp_async16_cg(dst + (x / PER) * LD + 4 * (x % PER), src + 4 * x);
 }
+// How a call's chunk states lie: a sequence has nc chunks at most, a head's states one behind the other ([N, H, NC]); or, by
+// row, packed sequences' in the order of their tokens ([slot, H]), so that they take the room of the tokens and not of N
+// sequences of the longest one. Sequence n's slots start at row0 / 64 + n: its ceil(len / 64) chunks end in front of
+// (row0 + len) / 64 + n + 1, where the next one's start.
+struct Chunks {
+    int nc, by_row;
+};
+__device__ __forceinline__ long long state_index(const Seqs& s, const Chunks& k, int n, int h, long long begin, int c) {
+    return k.by_row ? (begin / C32 + n + c) * s.H + h : ((long long)n * s.H + h) * k.nc + c;
+}
 struct Unit {
     int n, h, c, len, valid;
     long long row0, state;   // first token row; index of the chunk's state
 };
 // Blocks are (sequence, head, chunk), chunk fastest. False for a chunk behind its sequence's end.
-__device__ __forceinline__ bool unit_of(const Seqs& s, int nc, Unit* u) {
+__device__ __forceinline__ bool unit_of(const Seqs& s, const Chunks& k, Unit* u) {
     const int x = blockIdx.x;
-    u->c = x % nc;
-    u->h = (x / nc) % s.H;
-    u->n = x / nc / s.H;
+    u->c = x % k.nc;
+    u->h = (x / k.nc) % s.H;
+    u->n = x / k.nc / s.H;
     long long begin;
     u->len = linear::seq_span(s, u->n, &begin, &g_linear32_error);
     u->valid = min(C32, u->len - u->c * C32);
     u->row0 = begin + (long long)u->c * C32;
-    u->state = x;
+    u->state = state_index(s, k, u->n, u->h, begin, u->c);
     return u->valid > 0;
 }
 
 struct StateJob {
     const void *y, *z;
-    float* states;       // [N, H, NC, Dk, Dv]
+    float* states;       // [state index, Dk, Dv]
     const float* start;  // [N, H, Dk, Dv] or null
     float* end;          // or null
     int rev;
@@ -148,13 +158,13 @@ struct StateJobs {
 };
 
 template <int DK, int DV>
-__global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, const float* __restrict__ log_decay, StateJobs jobs) {
+__global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, Chunks k, const float* __restrict__ log_decay, StateJobs jobs) {
     constexpr int LY = DK + 8, LZ = DV + 8;   // 8-column shift a row: the k-major fragment reads meet no bank twice
     extern __shared__ float sm[];
     float *Y = sm, *Z = sm + C32 * LY;
     const StateJob& job = jobs.job[blockIdx.y];
     Unit u;
-    if (!unit_of(s, nc, &u)) return;
+    if (!unit_of(s, k, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
     load_rows<DK, LY>(Y, job.y, u.row0, u.valid, s.H, u.h);
     load_rows<DV, LZ>(Z, job.z, u.row0, u.valid, s.H, u.h);
@@ -172,7 +182,7 @@ __global__ void __launch_bounds__(NT32) chunk_states_kernel(Seqs s, int nc, cons
 }
 
 // One thread per state element and head: the chunks in order, each contribution replaced by the state in front of it.
-__global__ void __launch_bounds__(256) join_states_kernel(Seqs s, int nc, const float* __restrict__ log_decay, StateJobs jobs) {
+__global__ void __launch_bounds__(256) join_states_kernel(Seqs s, Chunks k, const float* __restrict__ log_decay, StateJobs jobs) {
     const StateJob& job = jobs.job[blockIdx.y];
     const int dd = s.Dk * s.Dv;
     const int per = dd / 256;
@@ -183,7 +193,8 @@ __global__ void __launch_bounds__(256) join_states_kernel(Seqs s, int nc, const 
     const float l2 = linear::log2_decay(log_decay, h);
     const int mine = linear::pieces(len, C32);
     float S = job.start ? job.start[(size_t)head * dd + e] : 0.f;
-    float* st = job.states + (size_t)head * nc * dd + e;
+    float* st = job.states + (size_t)state_index(s, k, n, h, begin, 0) * dd + e;
+    const size_t step = (size_t)dd * (k.by_row ? s.H : 1);   // from a chunk's state to the next one's
     const float whole = linear::decay_pow(l2, C32), last = linear::decay_pow(l2, len - (mine - 1) * C32);
     constexpr int AHEAD = 8;   // loads in flight a thread
     for (int c0 = 0; c0 < mine; c0 += AHEAD) {
@@ -191,13 +202,13 @@ __global__ void __launch_bounds__(256) join_states_kernel(Seqs s, int nc, const 
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int c = job.rev ? mine - 1 - (c0 + i) : c0 + i;
-            x[i] = c0 + i < mine ? st[(size_t)c * dd] : 0.f;
+            x[i] = c0 + i < mine ? st[c * step] : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             if (c0 + i >= mine) break;
             const int c = job.rev ? mine - 1 - (c0 + i) : c0 + i;
-            st[(size_t)c * dd] = S;
+            st[c * step] = S;
             S = fmaf(c == mine - 1 ? last : whole, S, x[i]);
         }
     }
@@ -223,7 +234,7 @@ struct OutTiles {
 };
 
 template <int DR, int DZ>
-__global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const float* __restrict__ log_decay, OutJobs jobs) {
+__global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, Chunks k, const float* __restrict__ log_decay, OutJobs jobs) {
     using L = OutTiles<DR, DZ>;
     constexpr int LX = L::LX, LZ = L::LZ, LP = L::LP;
     extern __shared__ float sm[];
@@ -231,7 +242,7 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const f
     __shared__ float pw[C32 + 1];
     const OutJob& job = jobs.job[blockIdx.y];
     Unit u;
-    if (!unit_of(s, nc, &u)) return;
+    if (!unit_of(s, k, &u)) return;
     const float l2 = linear::log2_decay(log_decay, u.h);
     const float* state = job.states + (size_t)u.state * DR * DZ;
     load_rows<DR, LX>(X, job.x, u.row0, u.valid, s.H, u.h);
@@ -268,58 +279,63 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, int nc, const f
     });
 }
 
-int chunks_of(const Seqs& s) { return linear::pieces(s.T, C32); }
+// The smaller of the two layouts: by row, sequences of much the same length would take more.
+Chunks chunks_of(const Seqs& s, bool packed) {
+    const int nc = linear::pieces(s.T, C32);
+    return Chunks{nc, packed && s.Ttot / C32 + s.N < (long long)s.N * nc};
+}
+size_t states_of(const Seqs& s, const Chunks& k) { return (size_t)s.H * (k.by_row ? s.Ttot / C32 + s.N : (long long)s.N * k.nc); }
 
 template <int DK, int DV>
-cudaError_t states(const LinearArgs& a, int nc, const StateJobs& jobs, int n, cudaStream_t s) {
+cudaError_t states(const LinearArgs& a, const Chunks& k, const StateJobs& jobs, int n, cudaStream_t s) {
     const int smem = (int)sizeof(float) * C32 * (DK + 8 + DV + 8);
     cudaError_t e = cudaFuncSetAttribute(chunk_states_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TraceScope trace(K_LINEAR_STATES, s);
-    chunk_states_kernel<DK, DV><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    chunk_states_kernel<DK, DV><<<dim3(a.seq.N * a.seq.H * k.nc, n), NT32, smem, s>>>(a.seq, k, a.log_decay, jobs);
     return cudaGetLastError();
 }
 template <int DR, int DZ>
-cudaError_t outputs(const LinearArgs& a, int nc, const OutJobs& jobs, int n, cudaStream_t s) {
+cudaError_t outputs(const LinearArgs& a, const Chunks& k, const OutJobs& jobs, int n, cudaStream_t s) {
     const int smem = (int)sizeof(float) * OutTiles<DR, DZ>::FLOATS;
     cudaError_t e = cudaFuncSetAttribute(chunk_out_kernel<DR, DZ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     TraceScope trace(K_LINEAR_OUT, s);
-    chunk_out_kernel<DR, DZ><<<dim3(a.seq.N * a.seq.H * nc, n), NT32, smem, s>>>(a.seq, nc, a.log_decay, jobs);
+    chunk_out_kernel<DR, DZ><<<dim3(a.seq.N * a.seq.H * k.nc, n), NT32, smem, s>>>(a.seq, k, a.log_decay, jobs);
     return cudaGetLastError();
 }
 
 template <int DK, int DV>
 cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
-    const int nc = chunks_of(a.seq);
-    const size_t set = (size_t)a.seq.N * a.seq.H * nc * DK * DV;
+    const Chunks k = chunks_of(a.seq, a.seq.cu != nullptr);
+    const size_t set = states_of(a.seq, k) * DK * DV;
     float* w = static_cast<float*>(a.ws);
     StateJobs sj{};
     int n = 0;
     sj.job[n++] = StateJob{a.k, a.v, w, a.S0, bwd ? nullptr : a.ST, 0};
     if (bwd) sj.job[n++] = StateJob{a.q, a.dout, w + set, a.dST, a.dS0, 1};
-    cudaError_t e = nc ? states<DK, DV>(a, nc, sj, n, s) : cudaSuccess;
+    cudaError_t e = k.nc ? states<DK, DV>(a, k, sj, n, s) : cudaSuccess;
     if (e != cudaSuccess) return e;
     {
         TraceScope trace(K_LINEAR_JOIN, s);
-        join_states_kernel<<<dim3(a.seq.N * a.seq.H * (DK * DV / 256), n), 256, 0, s>>>(a.seq, nc, a.log_decay, sj);
-        if ((e = cudaGetLastError()) != cudaSuccess || !nc) return e;
+        join_states_kernel<<<dim3(a.seq.N * a.seq.H * (DK * DV / 256), n), 256, 0, s>>>(a.seq, k, a.log_decay, sj);
+        if ((e = cudaGetLastError()) != cudaSuccess || !k.nc) return e;
     }
     OutJobs oj{};
     if (!bwd) {
         oj.job[0] = OutJob{a.q, a.k, a.v, w, a.o, 0, 0};
-        return outputs<DK, DV>(a, nc, oj, 1, s);
+        return outputs<DK, DV>(a, k, oj, 1, s);
     }
     oj.job[0] = OutJob{a.dout, a.v, a.k, w, a.dq, 0, 1};
     oj.job[1] = OutJob{a.v, a.dout, a.q, w + set, a.dk, 1, 1};
     const OutJob dv{a.k, a.q, a.dout, w + set, a.dv, 1, 0};
     if constexpr (DK == DV) {   // one kernel shape: one launch
         oj.job[2] = dv;
-        return outputs<DK, DV>(a, nc, oj, 3, s);
+        return outputs<DK, DV>(a, k, oj, 3, s);
     }
-    if ((e = outputs<DV, DK>(a, nc, oj, 2, s)) != cudaSuccess) return e;
+    if ((e = outputs<DV, DK>(a, k, oj, 2, s)) != cudaSuccess) return e;
     oj.job[0] = dv;
-    return outputs<DK, DV>(a, nc, oj, 1, s);
+    return outputs<DK, DV>(a, k, oj, 1, s);
 }
 
 template <int DK>
@@ -342,8 +358,8 @@ cudaError_t run_dk(const LinearArgs& a, bool bwd, cudaStream_t s) {
 
 }  // namespace
 
-size_t linear32_workspace(const Seqs& s, bool backward) {
-    return (size_t)s.N * s.H * chunks_of(s) * s.Dk * s.Dv * sizeof(float) * (backward ? 2 : 1);
+size_t linear32_workspace(const Seqs& s, bool packed, bool backward) {
+    return states_of(s, chunks_of(s, packed)) * s.Dk * s.Dv * sizeof(float) * (backward ? 2 : 1);
 }
 
 cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {

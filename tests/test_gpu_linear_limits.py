@@ -50,3 +50,29 @@ def test_every_record_is_named():
     assert binding.gdn2_device_status() == binding.GDN2_ERR_INVALID
     assert all(s in binding.last_error() for s in ("slots", "Tmax", "axes")), binding.last_error()
     assert binding.gdn2_device_status() == binding.GDN2_OK
+
+
+# one long sequence among many of 0 and 1 tokens (states by row), and sequences of one length (states by sequence), both with
+# a workspace of just the size asked for
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths", [[1, 0, 900, 1, 1, 0, 65, 0, 64, 1, 63, 0], [64] * 5, [129, 128, 127]])
+def test_packed_workspace_is_enough(dtype, lengths):
+    N, H, Dk, Dv = len(lengths), 2, 32, 64
+    x, d, cu = packed_case(lengths, H, Dk, Dv, dtype, 72, tail=3)
+    code = {"f32": binding.GDN2_F32, "bf16": binding.GDN2_BF16}[dtype]
+    args, Tmax, Ttot = (d["q"], d["k"], d["v"], d["g"]), max(lengths), sum(lengths) + 3
+    sizes = [binding.gdn2_linear_varlen_workspace_size(op, N, Tmax, Ttot, H, Dk, Dv, code) for op in (binding.GDN2_OP_FWD, binding.GDN2_OP_BWD)]
+    rooms = [torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device="cuda") for n in sizes]
+    o, ST = binding.gdn2_linear_varlen_fwd(*args, cu, Tmax, d["S0"], ws=rooms[0][:sizes[0]])
+    g = binding.gdn2_linear_varlen_bwd(*args, d["do"], cu, Tmax, d["S0"], d["dST"], ws=rooms[1][:sizes[1]])
+    assert binding.gdn2_device_status() == binding.GDN2_OK, binding.last_error()
+    assert all(bool((r[n:] == 0x5a).all()) for r, n in zip(rooms, sizes))
+    for i, n in enumerate(lengths):   # each sequence alone, bit for bit
+        at = slice(sum(lengths[:i]), sum(lengths[:i + 1]))
+        one = [d[m][at][None].contiguous() for m in ("q", "k", "v")] + [d["g"]]
+        o1, ST1 = binding.gdn2_linear_fwd(*one, d["S0"][i:i + 1])
+        g1 = binding.gdn2_linear_bwd(*one, d["do"][at][None].contiguous(), d["S0"][i:i + 1], d["dST"][i:i + 1])
+        if dtype == "f32":
+            assert torch.equal(o[at], o1[0]) and torch.equal(ST[i:i + 1], ST1), i
+            assert all(torch.equal(g[m][at], g1[m][0]) for m in ("dq", "dk", "dv")) and torch.equal(g["dS0"][i:i + 1], g1["dS0"]), i
+    check_packed(x, d, cu, lengths, Tmax, dtype)

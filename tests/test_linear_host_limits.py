@@ -59,14 +59,50 @@ def test_plans_cover_every_length(plan):
 def test_a_loose_bound_counts_as_the_rows(L, dt, Tmax, H):
     """What a packed call needs goes by its tensor where the bound is looser (the calls stop at the missing workspace)."""
     N, Ttot = 3, 300
-    for op, bwd in ((0, False), (2, True)):
-        need = L.gdn2_linear_workspace_size(op, N, Ttot, H, 64, 64, dt)
-        tail = (H, 64, 64, dt, P, need - 256, None)
-        if need == 0:   # many heads are not cut: nothing is needed, and nothing would stop the call
-            assert dt == 1 and H == 200
-            continue
-        if bwd:
-            rc = L.gdn2_linear_varlen_bwd(P, P, P, P, P, N, Tmax, Ttot, None, P, None, P, P, P, None, *tail)
-        else:
-            rc = L.gdn2_linear_varlen_fwd(P, P, P, P, P, N, Tmax, Ttot, None, P, None, *tail)
-        assert rc == 3 and b"needs %d workspace" % need in L.gdn2_last_error(), L.gdn2_last_error()
+    for bwd in (False, True):
+        said = []
+        for bound in (Ttot, Tmax):
+            tail = (H, 64, 64, dt, None, 0, None)
+            if dt == 1 and H == 200:   # many heads are not cut: nothing is needed, and the missing o stops the call
+                rc = L.gdn2_linear_varlen_fwd(P, P, P, P, P, N, bound, Ttot, None, None, None, *tail)
+            elif bwd:
+                rc = L.gdn2_linear_varlen_bwd(P, P, P, P, P, N, bound, Ttot, None, P, None, P, P, P, None, *tail)
+            else:
+                rc = L.gdn2_linear_varlen_fwd(P, P, P, P, P, N, bound, Ttot, None, P, None, *tail)
+            said.append((rc, L.gdn2_last_error()))
+        assert said[0] == said[1] and said[0][0] in (1, 3) and b"too large" not in said[0][1], said
+
+
+# ------------------------------------------------------------------ workspace of packed calls
+
+def _packed(L, bwd, N, Tmax, Ttot, H, Dk, Dv, dt, wsb):
+    tail = (H, Dk, Dv, dt, P, wsb, None)
+    if bwd:
+        return L.gdn2_linear_varlen_bwd(P, P, P, P, P, N, Tmax, Ttot, None, P, None, P, P, P, None, *tail)
+    return L.gdn2_linear_varlen_fwd(P, P, P, P, P, N, Tmax, Ttot, None, P, None, *tail)
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("op,bwd", [(0, False), (2, True)])
+def test_packed_workspace_goes_by_the_rows(L, dt, op, bwd):
+    size, dense = L.gdn2_linear_varlen_workspace_size, L.gdn2_linear_workspace_size
+    sets = 2 if bwd else 1
+    for N, Tmax, Ttot, H, Dk, Dv in ((24, 16384, 20000, 16, 128, 128), (3, INT_MAX, 300, 2, 64, 32), (1, 1, 1, 1, 16, 16),
+                                     (500, 2000, 2499, 2, 64, 64), (8, 64, 512, 2, 64, 64), (4, 100, 4000, 2, 32, 64)):
+        need = size(op, N, Tmax, Ttot, H, Dk, Dv, dt)
+        assert need % 256 == 0 and need <= dense(op, N, min(Tmax, Ttot), H, Dk, Dv, dt)
+        for looser in (Ttot, INT_MAX):
+            assert size(op, N, max(Tmax, looser), Ttot, H, Dk, Dv, dt) >= need
+        if dt == 0:
+            states = min(Ttot // 64 + N, N * -(-min(Tmax, Ttot) // 64))
+            assert need == -(-states * H * Dk * Dv * 4 * sets // 256) * 256, (N, Tmax, Ttot)
+        # the call asks for just that
+        if need:
+            assert _packed(L, bwd, N, Tmax, Ttot, H, Dk, Dv, dt, need - 1) == 3
+            assert b"needs %d workspace" % need in L.gdn2_last_error()
+    # one long sequence among short ones, in 32 bits: a state for each 64 rows, not 24 sequences of the longest
+    assert size(op, 24, 16384, 20000, 16, 128, 128, 0) == 336 * 16 * 65536 * sets
+    for bad in ((1, 2, 8, 10, 1, 64, 64, dt), (op, 0, 8, 10, 1, 64, 64, dt), (op, 2, -1, 10, 1, 64, 64, dt),
+                (op, 2, 8, -1, 1, 64, 64, dt), (op, 2, 8, 10, 1, 48, 64, dt), (op, 2, 8, 1 << 31, 1, 64, 64, dt),
+                (op, 2, 8, 10, 1, 64, 64, 7)):
+        assert size(*bad) == 0
