@@ -61,6 +61,9 @@
  *     test hook of the forward's two-launch form: the producer launch is left
  *     out, so the consumers' ready-flag waits run out and gdn2_device_status
  *     reports GDN2_ERR_TIMEOUT; outputs are then not valid.
+ *     GDN2_TEST_SKIP_LINEAR_ROLE (1 to 5) is one of the bf16 linear attention:
+ *     one of its kernel's roles (1 loads, 2 products, 3 pairs, 4 values,
+ *     5 state) does nothing and the others' waits give up after 5 ms.
  *     With few heads (B*H <= 32) and long sequences (at least 64 chunks) each
  *     head's chunks are cut into 4 to 8 segments that run on separate CTAs
  *     (the segments' affine state maps, a prefix over them, then the segments

@@ -165,6 +165,10 @@ static bool env_flag(const char* name) {
 }
 bool cooperative_disabled() { return env_flag("GDN2_NO_COOPERATIVE"); }
 bool test_skip_producers() { return env_flag("GDN2_TEST_SKIP_PRODUCERS"); }
+int test_skip_linear_role() {
+    const char* v = getenv("GDN2_TEST_SKIP_LINEAR_ROLE");
+    return v && v[0] >= '1' && v[0] <= '5' && v[1] == 0 ? v[0] - '0' : 0;
+}
 bool split_disabled() { return env_flag("GDN2_NO_SPLIT"); }
 }  // namespace gdn2
 

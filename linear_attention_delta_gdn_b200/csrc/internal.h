@@ -141,6 +141,7 @@ class TraceScope {
 // their producer and consumer work as two ordinary launches instead of one cooperative launch.
 bool cooperative_disabled();
 bool test_skip_producers();   // host-side fault injection for the forward's two-launch form
+int test_skip_linear_role();  // the same for linear_chunk_kernel: the number of a role that does nothing, 0 for none
 // The kernels' error words on the current device; gdn2_device_status reads and clears them (device_records.h has the bits).
 cudaError_t chunk_fwd_error_word(unsigned int** word);
 cudaError_t chunk_bwd_error_word(unsigned int** word);
