@@ -371,6 +371,9 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
  * NaN and infinity in a token reach every output of the chunk of 128 tokens it
  * lies in, earlier ones too, and the states behind it (before it, for the
  * backward); they never reach another sequence.
+ * Range: a product of three inputs (q k v, and in the backward dout v k and so on)
+ * summed over a chunk stays finite up to 2^96 in bf16, where heads of a_h >= 1/4
+ * are weighted in two factors of up to 2^32, and up to 2^127 in float32.
  * Packed sequences (the varlen calls): token tensors [Ttot, H, D] and
  * cu_seqlens [N + 1] int32 in device memory, as for gdn2_varlen_fwd, but read
  * and written in place: nothing is padded. A sequence of no tokens hands S0 to

@@ -358,6 +358,7 @@ __device__ void issue_products(const Params& p, unsigned char* sm, uint32_t tm, 
 
 // Mild decays keep a part of the pair weights for the outputs (weigh_pairs).
 constexpr float MILD = -2.f;   // log2 of the decay
+constexpr int MIDDLE = 16;     // of a warp's 32 rows: the power of the decay that row and column part differ by at most
 // A chunk's outputs, 32 rows a warp: o = f O1 + e O2 with f the power between the state's border and the row, e the row
 // part of the pair weights.
 struct Out {
@@ -372,7 +373,7 @@ __device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uin
     const bool rev = q.p->rev;
     unsigned char* Ob = sm + K::OFF_O + w * (K::OB / 4);   // this warp's 32 rows
     const float f = linear::decay_pow(q.l2, rev ? max(0, q.valid - 1 - orow) : orow + 1);
-    const float e = q.l2 >= MILD ? linear::decay_pow(q.l2, rev ? 31 - lane : lane) : 1.f;
+    const float e = q.l2 >= MILD ? exp2f(q.l2 * (float)((rev ? 31 - lane : lane) - MIDDLE)) : 1.f;
     const uint32_t quarter = (uint32_t)(32 * w) << 16;
     if (lane == 0) bulk_wait_read();   // the last store has read the staging rows
     if (!warp_wait(&b.o2_done[n & 1], (n >> 1) & 1)) return false;
@@ -418,10 +419,12 @@ __device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uin
 
 // Row i = 32 w + lane against column blocks of 32, those on the causal side.
 //
-// Mild decays (a >= 1/4, MILD): a^|i-j| = a^(row part) a^(column part), the row part (lane, or 31 - lane backwards) left
-// to the outputs, the column part 32 |w - jb| -+ j + const between -31 and 96: one value a column for all lanes, read
-// four at a time, and growing to 2^62 at most, which P (8-bit exponents) and the sum take. pw[pos] holds it by position.
-// Stronger decays would overflow it: their weights are read by distance, pw[128 + i - j], 0 off the causal side.
+// Mild decays (a >= 1/4, MILD): a^|i-j| = a^(row part) a^(column part), the row part (lane - 16, or 15 - lane backwards)
+// left to the outputs, the column part 32 |w - jb| -+ j + const between -15 and 112: one value a column for all lanes,
+// read four at a time. pw[pos] holds it by position. P and its sum with Z are then up to 2^30 times (the last columns of a
+// diagonal block) or 2^-32 (its first) what the outputs take of them, 32 bits of range that 2^127 has to spare; with the
+// row part starting at 0 it was 2^62, and outputs of 2^84 became infinite. Stronger decays would grow further: their
+// weights are read by distance, pw[128 + i - j], 0 off the causal side.
 template <int DRP>
 __device__ void weigh_pairs(const Params& p, unsigned char* sm, uint32_t tm, Bars& b, float* pw) {
     using K = Cfg<DRP, false>;
@@ -435,7 +438,7 @@ __device__ void weigh_pairs(const Params& p, unsigned char* sm, uint32_t tm, Bar
         const bool rev = t.p->rev, mild = t.l2 >= MILD;
         if (named_sync_or(2, 128, !ok)) break;       // the last item's weights have been read
         if (mild) {
-            pw[rev ? 127 - tid : tid] = exp2f(t.l2 * (float)(96 - tid));
+            pw[rev ? 127 - tid : tid] = exp2f(t.l2 * (float)(96 + MIDDLE - tid));
         } else {
             pw[128 + (rev ? -tid : tid)] = linear::decay_pow(t.l2, tid);
             if (tid) pw[128 + (rev ? tid : -tid)] = 0.f;

@@ -7,7 +7,7 @@ import torch
 from linear_attention_delta_gdn_b200 import binding
 from linear_attention_delta_gdn_b200.inputs import to_f64
 from oracle import linear as lin
-from test_gpu_linear import built, check_states, check_tokens, packed_case  # noqa: F401 (built: the module's fixture)
+from test_gpu_linear import built, check_dense, check_states, check_tokens, make, packed_case  # noqa: F401 (built: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,24 @@ def test_packed_workspace_is_enough(dtype, lengths):
             assert torch.equal(o[at], o1[0]) and torch.equal(ST[i:i + 1], ST1), i
             assert all(torch.equal(g[m][at], g1[m][0]) for m in ("dq", "dk", "dv")) and torch.equal(g["dS0"][i:i + 1], g1["dS0"]), i
     check_packed(x, d, cu, lengths, Tmax, dtype)
+
+
+# either side of a decay of 1/4 a token (-2 ln 2 = -1.38629436), where the pairs' weights change from products of a row's and a
+# column's part, largest there, to one read by distance
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decays_around_a_quarter(dtype, D):
+    x, d = make((1, 333), 1, 8, D, D, dtype, 73, [-1.0, -1.2, -1.386, -1.3862943, -1.3862944, -1.3863, -1.5, -2.5])
+    check_dense(x, d, dtype)
+
+
+# Large and small numbers: outputs are products of three inputs, 2^84 to 2^92 here (or their inverses), and 32 bits hold
+# 2^127. What a weight's two parts add on the way (2^30 either way at the strongest decay that has them) must fit, too.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [28, -28])
+def test_large_and_small_numbers(dtype, scale):
+    x, d = make((1, 333), 1, 5, 64, 64, dtype, 74, [-1.386, -1.2, -0.7, 0.0, -3.0])
+    for n, times in (("q", 1), ("k", 1), ("v", 1), ("do", 1), ("S0", 2), ("dST", 2)):
+        x[n] = x[n] * 2.0 ** (scale * times)   # a power of two: exact
+        d[n] = x[n].cuda()
+    check_dense(x, d, dtype)
