@@ -434,14 +434,16 @@ gdn2_status gdn2_linear_decode_step(const void* q, const void* k, const void* v,
  *                    are taken where they lie
  *   q_out, k_out   : [B, T, Hq, D] and [B, T, Hk, D] dt; may be q and k where
  *                    those are contiguous (each row is read before it is written)
- *   positions      : [num_axes, B, T] int32 (pos_bytes = 4) or int64 (8), any value
- *   inv_freq       : [pairs] float32 ;  axes : [pairs] int32 or NULL (all 0)
+ *   positions      : [num_axes, B, T] int32 (pos_bytes = 4) or int64 (8), any sign
+ *   inv_freq       : [pairs] float32, any sign ;  axes : [pairs] int32 or NULL (all 0)
  *   pairs          : 1 .. D / 2
  *   q_weight, k_weight : [D] float32, or NULL for a norm without a weight
- * The angle is reduced in 64 bits, so far positions turn as exactly as near
- * ones. An axis outside [0, num_axes) turns nothing and is reported by
- * gdn2_device_status (GDN2_ERR_INVALID, "axes"). D in {16, 32, 64, 128}. An L2
- * norm x / sqrt(sum(x^2) + e) is the weight 1 / sqrt(D) with eps = e / D.
+ * The angle is a product in 64-bit fractions of a turn, off by |position| 2^-63
+ * turns at most: no more than a 32-bit angle's rounding up to positions of 2^38
+ * (every int32 one), 7e-7 rad at 2^40, and without meaning near 2^63. An axis
+ * outside [0, num_axes) turns nothing and is reported by gdn2_device_status
+ * (GDN2_ERR_INVALID, "axes"). D in {16, 32, 64, 128}. An L2 norm
+ * x / sqrt(sum(x^2) + e) is the weight 1 / sqrt(D) with eps = e / D.
  *
  * gdn2_qk_norm_rope_bwd: dq, dk (contiguous, as the outputs; they may be dq_out
  * and dk_out) from the forward's inputs and the outputs' gradients, and with a

@@ -14,8 +14,9 @@
 // Measured: 4 x 4096 tokens of 16 + 16 heads of 128 take 54 us, 4.9 TB/s (76% of the copy rate); 2 x 3999 tokens of 16 + 4
 // heads with the backward and both weights' gradients 58 us (the forward 24, the backward 35: loads of few rows a token
 // to wait for); 64 tokens of one serving step 3.6 us, the latency of the loads.
-// Far positions: the angle is a whole-number product modulo one turn, so a position of millions (or of 2^40) keeps the
-// error of a small one (a 32-bit product is off by 0.06 at a million).
+// Far positions: the angle is a whole-number product modulo one turn, off by |position| 2^-63 turns at most, whatever the
+// sign of the position or the frequency: below a 32-bit angle's own rounding up to 2^38, 7e-7 rad at 2^40 (a 32-bit product
+// is off by 0.06 rad at a million).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -132,13 +133,16 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // Turns per position as a 64-bit fraction (whole turns do not count): the product with 1 / 2 pi as a double and its
-// rest, so it is right to its last bit.
+// rest, each off by one unit of 2^-64 at most. Of the size, negated as a whole number: a small negative double
+// brought to [0, 1) would keep 53 bits of its difference to 1.
 __device__ __forceinline__ unsigned long long turns_of(float inv_freq) {
-    const double f = inv_freq;
+    const double f = fabsf(inv_freq);
     double turns = f * 0.15915494309189535;
     const double rest = fma(f, 0.15915494309189535, -turns) + f * -9.839338337591243e-18;
     turns -= floor(turns);
-    return __double2ull_rz(turns * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(rest * 18446744073709551616.0);
+    const unsigned long long units =
+        __double2ull_rz(turns * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(rest * 18446744073709551616.0);
+    return inv_freq < 0.f ? 0ull - units : units;
 }
 // The thread's index, read once (the compiler would read the special register again wherever registers are short, and a
 // read takes as long as a shuffle).
@@ -168,7 +172,7 @@ __device__ __forceinline__ void make_pairs(const QkRopeArgs& a, Pairs& q) {
     __syncthreads();
 }
 // cos and sin of token t's angles for this lane's slots; `cs` is the warp's own. pos * turns wraps at whole turns by
-// itself, so the angle is off by |pos| 2^-64 turns before it rounds to 32 bits.
+// itself, so the angle is off by |pos| times what a turn's fraction is before it rounds to 32 bits.
 template <typename T, int D, int VEC>
 __device__ __forceinline__ void make_angles(const QkRopeArgs& a, const Pairs& q, long long t, int lane, float2* cs,
                                             float2 (&mine)[RowLayout<D, VEC>::SPL][VEC]) {
