@@ -47,8 +47,28 @@ class LayerGates(torch.autograd.Function):
         return dz, da, None, None
 
 
-class Gdn2Layer(torch.nn.Module):
-    """``y, S_T = layer(x, S0)`` for x [B, T, d_model]; bf16 (tensor-core operator path at d = 128) or fp32."""
+class _Float32Parts(torch.nn.Module):
+    """A module whose members named in ``_float32`` keep their 32 bits when it is cast (``.to(torch.bfloat16)`` and the like):
+    the kernels take them in no other type, and a frequency or decay that has been through 8 bits is another one."""
+    _float32 = ()
+
+    def _apply(self, *args, **kwargs):
+        before = {n: (t.detach(), None if t.grad is None else t.grad.detach())
+                  for n in self._float32 for t in (getattr(self, n),) if t.dtype == torch.float32}
+        super()._apply(*args, **kwargs)
+        for n, (data, grad) in before.items():
+            t = getattr(self, n)
+            if t.dtype != torch.float32:   # cast: the same bits again, where the module now is
+                t.grad = None
+                t.data = data.to(t.device)
+                t.grad = None if grad is None else grad.to(t.device)
+        return self
+
+
+class Gdn2Layer(_Float32Parts):
+    """``y, S_T = layer(x, S0)`` for x [B, T, d_model]; bf16 (tensor-core operator path at d = 128) or fp32 (the projections'
+    type, also by ``.to``; the decay bias stays float32)."""
+    _float32 = ("a_bias",)
 
     def __init__(self, d_model: int, n_heads: int, d_k: int = 128, d_v: int = 128, chunk: int = 64,
                  dtype=torch.bfloat16, device=None, decay_bias: float = -4.0):
@@ -70,7 +90,7 @@ class Gdn2Layer(torch.nn.Module):
         return y, ST
 
 
-class DecayLinearAttentionLayer(torch.nn.Module):
+class DecayLinearAttentionLayer(_Float32Parts):
     """A linear-attention layer with one fixed decay per head:
 
         q, k = x W_qk per head,  RMS-normalised with a weight each, pairs of channels turned by the token's position
@@ -79,8 +99,10 @@ class DecayLinearAttentionLayer(torch.nn.Module):
     ``y, S_T = layer(x, S0, positions)`` for x [B, T, d_model], or packed [Ttot, d_model] with ``cu_seqlens`` and ``Tmax``;
     ``layer.step(x, positions, S, slots)`` for one token of each of B requests. ``pairs`` (d_k / 2 if not given) channel
     pairs turn; with ``sections`` pair by pair along several axes, positions then being [axes, ...]. ``log_decay`` [n_heads]
-    defaults to memories of 8 to 256 tokens. bf16 or fp32.
+    defaults to memories of 8 to 256 tokens. bf16 or fp32: the projections' type, also by ``.to``; the norms' weights, decays
+    and frequencies stay float32.
     """
+    _float32 = ("q_weight", "k_weight", "log_decay", "inv_freq")
 
     def __init__(self, d_model: int, n_heads: int, d_k: int = 128, d_v: int = 128, pairs: Optional[int] = None, sections=None,
                  base: float = 10000.0, eps: float = 1e-6, log_decay: Optional[torch.Tensor] = None, dtype=torch.bfloat16,
