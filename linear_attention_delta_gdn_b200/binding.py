@@ -772,6 +772,8 @@ class QkNormRope(torch.autograd.Function):
 def qk_norm_rope(q, k, positions, inv_freq, axes=None, q_weight=None, k_weight=None, eps: Optional[float] = 1e-6,
                  interleaved: bool = False):
     """Differentiable :func:`gdn2_qk_norm_rope_fwd` (gradients of q, k and the weights). Returns ``(q_out, k_out)``."""
+    if inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq has no gradient: pass it detached")
     return QkNormRope.apply(q, k, positions, inv_freq, axes, q_weight, k_weight, eps, interleaved)
 
 

@@ -106,3 +106,15 @@ def test_packed_workspace_goes_by_the_rows(L, dt, op, bwd):
                 (op, 2, 8, -1, 1, 64, 64, dt), (op, 2, 8, 10, 1, 48, 64, dt), (op, 2, 8, 1 << 31, 1, 64, 64, dt),
                 (op, 2, 8, 10, 1, 64, 64, 7)):
         assert size(*bad) == 0
+
+
+# ------------------------------------------------------------------ what has no gradient
+
+def test_frequencies_that_want_a_gradient_are_refused():
+    import torch
+    from linear_attention_delta_gdn_b200 import binding as b
+    x, pos, f = torch.zeros(1, 4, 2, 16), torch.zeros(1, 4, dtype=torch.int32), torch.ones(8, requires_grad=True)
+    with pytest.raises(ValueError, match="inv_freq has no gradient"):
+        b.qk_norm_rope(x, x, pos, f)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):   # nothing is lost there: on to the next check
+        b.qk_norm_rope(x, x, pos, f)
