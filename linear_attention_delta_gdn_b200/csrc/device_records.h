@@ -23,7 +23,7 @@ constexpr unsigned int ERR_WAIT = 8u;      // a bounded wait gave up
 struct DeviceRecords {
     unsigned int fwd, bwd;        // chunk_fwd_kernel, chunk_bwd_kernel: bits of waits, GDN2_DBG_BIT
     unsigned int varlen;          // packed-sequence copies
-    unsigned int linear;          // linear attention, both precisions
+    unsigned int linear;          // linear attention, both precisions: bits of packed calls and waits, GDN2_DBG_BIT
     unsigned int step, rope;
 };
 
@@ -54,6 +54,8 @@ inline gdn2_status describe_records(const DeviceRecords& r, char* text, size_t c
             "index check failed (debug build; the accesses it guarded were skipped): chunk_fwd_kernel bits "
             "0x%x, chunk_bwd_kernel bits 0x%x",
             r.fwd, r.bwd);
+    if (r.linear & GDN2_DBG_BIT)
+        add(GDN2_ERR_INVALID, "index check failed (debug build; the accesses it guarded were skipped): linear attention bits 0x%x", r.linear);
     const unsigned int packed = (r.varlen | r.linear) & (ERR_LONG | ERR_OUTSIDE);
     if (packed)
         add(GDN2_ERR_INVALID, "cu_seqlens: %s%s", (packed & ERR_LONG) ? "a sequence was longer than Tmax (cut) " : "",

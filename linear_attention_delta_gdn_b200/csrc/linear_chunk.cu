@@ -73,6 +73,7 @@ struct Params {
     const float* log_decay;
     int npass, dr, dz, slices;
     int nseg, cps;           // segments of a sequence at most, chunks of a segment
+    long long slots;         // of segments' states
     int items;
     int skipped;             // tests: a role that does nothing, so that the others' waits run out (0: none)
     uint32_t wait_ns;        // how long a wait lasts before it gives up
@@ -112,12 +113,14 @@ __device__ __noinline__ void find_item(const Params& p, uint32_t x, Item* t) {
         if (t->p->rev ? t->seg == 0 : t->seg >= last) t->c1 = t->c0;
     }
     t->l2 = linear::log2_decay(p.log_decay, t->h);
+    if (!GDN2_IN(g_linear_error, t->seg < p.nseg && t->c0 >= 0 && t->c0 <= t->c1 && t->c1 <= t->nc)) t->c1 = t->c0;
 }
-// Where a segment's own state lies. Sequence n's segments take the slots from row0 / S + n on, S the tokens of a segment:
+// Where a segment's own state lies (null if the debug build finds that it lies outside: nothing is read or written then). Sequence n's segments take the slots from row0 / S + n on, S the tokens of a segment:
 // ceil(len / S) of them never reach (row0 + len) / S + n + 1, where the next sequence's begin.
 template <int DRP>
 __device__ __forceinline__ float* segment_state(const Params& p, const Item& t, int seg) {
     const long long slot = t.row0 / ((long long)p.cps * CT) + t.n + seg;
+    if (!GDN2_IN(g_linear_error, slot >= 0 && slot < p.slots && seg >= 0 && seg < p.nseg)) return nullptr;
     return t.p->seg + ((slot * p.seq.H + t.h) * p.slices + t.slice) * (long long)(SL * DRP);
 }
 // The block's first item is found once, before the roles start (its loads and the first reads of the parameters take as
@@ -634,8 +637,9 @@ __device__ __forceinline__ void start_state(const Params& p, const Item& t, int 
                     S[j] = f * v.x; S[j + 1] = f * v.y; S[j + 2] = f * v.z; S[j + 3] = f * v.w;
                 }
         } else {   // columns contiguous over the rows
-            const float* src = first ? q.start + (head * p.dz + t.slice * SL) * p.dr + r
-                                     : segment_state<DRP>(p, t, o) + r;
+            const float* src = first ? q.start + (head * p.dz + t.slice * SL) * p.dr : segment_state<DRP>(p, t, o);
+            if (!src) continue;
+            src += r;
             const int step = first ? p.dr : DRP, cols = first ? p.dz - t.slice * SL : SL;
 #pragma unroll
             for (int j = 0; j < SL; ++j)
@@ -705,9 +709,10 @@ __device__ void carry_state(const Params& p, unsigned char* sm, uint32_t tm, Bar
         }
         if (!ok || !real) continue;
         if (STATES) {
-            float* dst = segment_state<DRP>(p, t, t.seg) + r;
+            if (float* dst = segment_state<DRP>(p, t, t.seg)) {
 #pragma unroll
-            for (int j = 0; j < SL; ++j) dst[j * DRP] = S[j];
+                for (int j = 0; j < SL; ++j) dst[j * DRP + r] = S[j];
+            }
         } else if (writes_end && r < p.dr) {
             float* dst = t.p->end + (((size_t)t.n * p.seq.H + t.h) * p.dr + r) * p.dz + t.slice * SL;
 #pragma unroll
@@ -849,6 +854,7 @@ cudaError_t run_group(const LinearArgs& a, const Group& g, const Cut& cut, cudaS
     p.slices = slices_of(g.dz);
     p.nseg = cut.nseg;
     p.cps = cut.cps;
+    p.slots = cut.slots;
     const long long items = (long long)cut.nseg * a.seq.N * a.seq.H * g.npass * p.slices;
     if (items > 2000000000ll) return cudaErrorInvalidConfiguration;
     p.items = (int)items;

@@ -124,6 +124,7 @@ __device__ __forceinline__ void load_state(float* dst, const float* src) {
 // (row0 + len) / 64 + n + 1, where the next one's start.
 struct Chunks {
     int nc, by_row;
+    long long total;   // states
 };
 __device__ __forceinline__ long long state_index(const Seqs& s, const Chunks& k, int n, int h, long long begin, int c) {
     return k.by_row ? (begin / C32 + n + c) * s.H + h : ((long long)n * s.H + h) * k.nc + c;
@@ -143,7 +144,7 @@ __device__ __forceinline__ bool unit_of(const Seqs& s, const Chunks& k, Unit* u)
     u->valid = min(C32, u->len - u->c * C32);
     u->row0 = begin + (long long)u->c * C32;
     u->state = state_index(s, k, u->n, u->h, begin, u->c);
-    return u->valid > 0;
+    return u->valid > 0 && GDN2_IN(g_linear32_error, u->state >= 0 && u->state < k.total);
 }
 
 struct StateJob {
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(256) join_states_kernel(Seqs s, Chunks k, cons
     long long begin;
     const int len = linear::seq_span(s, n, &begin, &g_linear32_error);
     const float l2 = linear::log2_decay(log_decay, h);
-    const int mine = linear::pieces(len, C32);
+    int mine = linear::pieces(len, C32);
+    if (mine && !GDN2_IN(g_linear32_error, mine <= k.nc && state_index(s, k, n, h, begin, mine - 1) < k.total)) mine = 0;
     float S = job.start ? job.start[(size_t)head * dd + e] : 0.f;
     float* st = job.states + (size_t)state_index(s, k, n, h, begin, 0) * dd + e;
     const size_t step = (size_t)dd * (k.by_row ? s.H : 1);   // from a chunk's state to the next one's
@@ -282,9 +284,10 @@ __global__ void __launch_bounds__(NT32) chunk_out_kernel(Seqs s, Chunks k, const
 // The smaller of the two layouts: by row, sequences of much the same length would take more.
 Chunks chunks_of(const Seqs& s, bool packed) {
     const int nc = linear::pieces(s.T, C32);
-    return Chunks{nc, packed && s.Ttot / C32 + s.N < (long long)s.N * nc};
+    const long long by_row = s.Ttot / C32 + s.N, by_sequence = (long long)s.N * nc;
+    const bool rows = packed && by_row < by_sequence;
+    return Chunks{nc, rows, s.H * (rows ? by_row : by_sequence)};
 }
-size_t states_of(const Seqs& s, const Chunks& k) { return (size_t)s.H * (k.by_row ? s.Ttot / C32 + s.N : (long long)s.N * k.nc); }
 
 template <int DK, int DV>
 cudaError_t states(const LinearArgs& a, const Chunks& k, const StateJobs& jobs, int n, cudaStream_t s) {
@@ -308,7 +311,7 @@ cudaError_t outputs(const LinearArgs& a, const Chunks& k, const OutJobs& jobs, i
 template <int DK, int DV>
 cudaError_t run(const LinearArgs& a, bool bwd, cudaStream_t s) {
     const Chunks k = chunks_of(a.seq, a.seq.cu != nullptr);
-    const size_t set = states_of(a.seq, k) * DK * DV;
+    const size_t set = (size_t)k.total * DK * DV;
     float* w = static_cast<float*>(a.ws);
     StateJobs sj{};
     int n = 0;
@@ -359,7 +362,7 @@ cudaError_t run_dk(const LinearArgs& a, bool bwd, cudaStream_t s) {
 }  // namespace
 
 size_t linear32_workspace(const Seqs& s, bool packed, bool backward) {
-    return states_of(s, chunks_of(s, packed)) * s.Dk * s.Dv * sizeof(float) * (backward ? 2 : 1);
+    return (size_t)chunks_of(s, packed).total * s.Dk * s.Dv * sizeof(float) * (backward ? 2 : 1);
 }
 
 cudaError_t linear32_launch(const LinearArgs& a, bool bwd, cudaStream_t s) {

@@ -111,3 +111,10 @@ def test_the_binding_asks_the_device_it_is_given(monkeypatch):
     monkeypatch.setattr(binding, "lib", Lib)
     assert binding.gdn2_device_status() == 0 and binding.gdn2_device_status("cuda:1") == 0
     assert asked == [(0, 100), (1, 101)] and current == [0]
+
+
+def test_an_index_check_of_the_linear_kernels(describe):
+    status, text = describe((0, 0, 0, DBG, 0, 0))
+    assert status == INVALID and text.startswith("index check") and "linear attention" in text
+    status, text = describe((0, 0, 0, DBG | 8 | 1, 0, 0))
+    assert status == TIMEOUT and all(s in text for s in ("linear_chunk_kernel", "index check", "Tmax"))
