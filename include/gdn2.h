@@ -366,11 +366,16 @@ gdn2_status gdn2_layer_gates_bwd(const void* z, const float* a_bias, const void*
  *                        and dS0 dST.
  * gdn2_linear_bwd gives the gradients of <dout, o> + <dST, S_T> from the
  * forward's inputs alone (nothing is kept by the forward); the three token
- * gradients must be given. o and the token gradients must not alias the inputs.
+ * gradients must be given. Outputs share memory with inputs and with one another
+ * only as said above.
  * Dk, Dv in {16, 32, 64, 128}, float32 or bf16, any T >= 0.
  * NaN and infinity in a token reach every output of the chunk of 128 tokens it
  * lies in, earlier ones too, and the states behind it (before it, for the
  * backward); they never reach another sequence.
+ * Precision (relative L2 against 64 bits, as measured): float32 within 2.2e-7, and
+ * sums in 32 bits throughout. In bf16 a chunk's pair weights and the state that its
+ * outputs read round to bf16: token outputs 2.3e-3, of which their own rounding is
+ * 1.7e-3; the float32 states take products of 2^-18, 3.3e-6.
  * Range: a product of three inputs (q k v, and in the backward dout v k and so on)
  * summed over a chunk stays finite up to 2^96 in bf16, where heads of a_h >= 1/4
  * are weighted in two factors of up to 2^32, and up to 2^127 in float32.

@@ -9,13 +9,14 @@
 // The state R lives in registers of one warpgroup in 32 bits. D does not depend on it, so the only thing one chunk
 // hands the next is R' = a^C R + D and its bf16 copy for O1.
 //
-// What bounds it: a chunk takes a block 1.8 us (3400 cycles), for rows of 64 as for 128 and for one block as for 128 of
+// What bounds it: a chunk takes a block 1.7 to 1.9 us (3400 to 3700 cycles), for rows of 64 as for 128 and for one block as for 128 of
 // them: the round trips between the roles. Its products are 1670 cycles of the tensor pipe alone (64 a K step at
 // N 128, 48 at N 64 from shared memory, 32 from TMEM); the pairs' warpgroup works 2800 (P 1300 and outputs 1300), the
 // values' 2200, the state's 1200; a chunk's tiles take 2400 from request to arrival, and X, held from its A to its O1 a
 // chunk later, has two stages. Measured: 72 us for 4 x 4096 tokens, 16 heads of 128 (273 MB, 58% of the copy rate; 30% of
 // the tensor pipe's cycles, 128 blocks), 279 us with the backward, 380 us for 65536 tokens of 16 heads from a stored
-// state (two launches).
+// state (two launches). The backward's launch alone takes 208 us: 384 items on 148 blocks, 41% of the tensor pipe's cycles,
+// 1.03 GB from L2 and 369 MB from memory for 268 MB of inputs.
 // Tried and not faster: Zh and Zl made before D is waited for (registers), Zh and Zl in two buffers with the outputs stored
 // from registers (76 us), three buffers of Z through TMA with rolled loops (74 us), X in three stages (79 us), P shared
 // between two warpgroups (90 us), A ahead of D (78 us), the product loops unrolled (73 us).
@@ -24,9 +25,9 @@
 // a 32-bit result, so g_j z_j goes into D as two bf16 terms, hi and the rest: 2^-18, where one term would leave 2^-9
 // in a state that every later token reads. Sums are 32-bit.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P and writes the
-// outputs; warpgroup 2 makes Zh and Zl; warpgroup 3 keeps the state. A block takes work items (sequence, head, column slice, segment, pass) in turn and
-// the warps run ahead of one another across items.
+// Warps: 0 loads (TMA), 1 issues the MMAs; warpgroup 1 turns A into P and writes the outputs; warpgroup 2 makes Zh and Zl;
+// warpgroup 3 keeps the state. A block takes work items (sequence, head, column slice, segment, pass) in turn and the
+// warps run ahead of one another across items.
 //
 // Few heads: a sequence's chunks are cut into segments of whole chunks, each an item of its own. A first launch leaves
 // the state that each segment's tokens alone make (k and v are read twice then); a segment's start is the sum of those
@@ -427,7 +428,8 @@ __device__ __forceinline__ bool write_outputs(const Params& p, const Out& q, uin
 // read four at a time. pw[pos] holds it by position. P and its sum with Z are then up to 2^30 times (the last columns of a
 // diagonal block) or 2^-32 (its first) what the outputs take of them, 32 bits of range that 2^127 has to spare; with the
 // row part starting at 0 it was 2^62, and outputs of 2^84 became infinite. Stronger decays would grow further: their
-// weights are read by distance, pw[128 + i - j], 0 off the causal side.
+// weights are read by distance, pw[128 + i - j], 0 off the causal side. With the row and column parts 4 x 4096 tokens of
+// 16 heads of 128 take 73 us (a = 0.9) to 79 (a = 0.252), by distance 89 (a = 0.249).
 template <int DRP>
 __device__ void weigh_pairs(const Params& p, unsigned char* sm, uint32_t tm, Bars& b, float* pw) {
     using K = Cfg<DRP, false>;

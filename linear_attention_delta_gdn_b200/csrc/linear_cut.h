@@ -28,7 +28,7 @@ struct Cut {
 inline long long most_items(long long heads, int nsm) { return 2 * heads + 4 * nsm; }
 inline bool may_cut(int T, long long heads, int nsm) { return T > CHUNK && heads < 4 * nsm; }
 
-// Time in chunks of one block (1.9 us): the fullest block's chunks and 4 more for each of its items' start and end, in
+// Time in chunks of one block (1.7 to 1.9 us): the fullest block's chunks and 4 more for each of its items' start and end, in
 // more than one segment also 1.5 for each segment that an item's start is summed from, and the launch before, whose chunks
 // cost half as much (a sequence's last segment has none there), with 3 for the launch itself. Sequences of one length go in
 // waves. Of packed ones only the sum of their lengths is known here: the fullest block is taken to have the mean and half

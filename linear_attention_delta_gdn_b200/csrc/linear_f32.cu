@@ -15,7 +15,8 @@
 //
 // This is the path for checks of a model's numerics; its work is the products' (three mma.sync for one, and the splitting
 // of each operand, 47% of the issue slots in chunk_out_kernel), its time that of the launches where there are few tokens:
-// training on 2 x 1001 tokens, 4 heads of 64, takes 59 us in six launches, 2 x 13 in the outputs of one pass.
+// training on 2 x 1001 tokens, 4 heads of 64, takes 59 us in six launches, 2 x 13 in the outputs of one pass. 4 x 4096
+// tokens of 16 heads of 128 take 1190 us forward and 2890 backward, where their bytes would take 82 and 164.
 #include <cuda_runtime.h>
 
 #include "chunk_common.cuh"

@@ -104,7 +104,9 @@ cudaError_t step(const LinearStepArgs& a, cudaStream_t s) {
 }
 template <typename Tin, int DK>
 cudaError_t step_columns(const LinearStepArgs& a, cudaStream_t s) {
-    // Few states: 32 columns a block, so that a small batch's states spread over more SMs.
+    // Few states: 32 columns a block, so that a small batch's states spread over more SMs. In a replayed graph, states of
+    // 128 x 128, 32 columns a block against all of them: 64 states 4.3 against 6.2 us, 128 states 6.3 both, 256 states 8.3
+    // against 6.6.
     const bool few = (long long)a.B * a.H * (a.Dv / 32) <= 2 * 148;
     if (a.Dv == 16) return step<Tin, DK, 16>(a, s);
     if (a.Dv == 32 || few) return step<Tin, DK, 32>(a, s);

@@ -430,7 +430,8 @@ cudaError_t run(const QkRopeArgs& a, float* ws, cudaStream_t s) {
     q_blocks = (int)(blocks < q_blocks ? blocks : q_blocks);
     k_blocks = (int)(blocks < k_blocks ? blocks : k_blocks);
     if (!a.dq) {
-        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share
+        // few tokens: their heads over several warps, as long as there are SMs without work and rows to share (1 to 64 tokens
+        // of 16 + 4 heads: 4.3 us in a replayed graph, 6.3 with a token's heads in one warp; from 256 tokens on the same)
         const int rows = ((a.Hq > a.Hk ? a.Hq : a.Hk) + RowLayout<D, VEC>::RPW - 1) / RowLayout<D, VEC>::RPW;
         const long long want = (148 + 2 * blocks - 1) / (2 * blocks);
         const int parts = (int)(want < rows ? want : rows);
@@ -451,7 +452,9 @@ cudaError_t run(const QkRopeArgs& a, float* ws, cudaStream_t s) {
 }
 template <typename T, int D>
 cudaError_t run_d(const QkRopeArgs& a, float* ws, cudaStream_t s) {
-    // as many pairs at a time as 16 bytes hold where the pairs divide so, else four, else one
+    // as many pairs at a time as 16 bytes hold where the pairs divide so, else four, else one. 4 x 4096 tokens of 16 + 4 heads
+    // of 128, forward / backward in us: bf16 64 pairs (eight) 38 / 63, 60 pairs (four) 47 / 63, 61 pairs (one) 78 / 121;
+    // fp32 60 pairs (four) 74 / 123, 61 pairs (one) 100 / 167.
     if (sizeof(T) == 2 && a.pairs % 8 == 0) {
         if constexpr (sizeof(T) == 2) return a.interleaved ? run<T, D, 8, true>(a, ws, s) : run<T, D, 8, false>(a, ws, s);
     }
