@@ -141,8 +141,9 @@ cudaError_t take_error_words(unsigned int (&taken)[ERROR_WORDS]) {
     }
     static std::mutex one_at_a_time;   // g_taken
     std::lock_guard<std::mutex> lock(one_at_a_time);
-    take_error_words_kernel<<<1, 32>>>(w);
-    const cudaError_t e = cudaGetLastError();
+    // (launched by the call that returns its own error: the last one recorded may be of something before)
+    void* args[] = {&w};
+    const cudaError_t e = cudaLaunchKernel(take_error_words_kernel, dim3(1), dim3(32), args, 0, nullptr);
     return e != cudaSuccess ? e : cudaMemcpyFromSymbol(taken, g_taken, sizeof(taken));
 }
 
