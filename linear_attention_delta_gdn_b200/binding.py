@@ -36,9 +36,9 @@ EXPORTS = ("gdn2_workspace_size", "gdn2_fwd", "gdn2_bwd", "gdn2_decode_step", "g
            "gdn2_trace_enable", "gdn2_trace_read", "gdn2_device_status", "gdn2_beta_workspace_size",
            "gdn2_beta_fwd", "gdn2_beta_bwd", "gdn2_varlen_workspace_size", "gdn2_varlen_fwd", "gdn2_varlen_bwd",
            "gdn2_fwd_map", "gdn2_bwd_map", "gdn2_state_affine", "gdn2_layer_gates_fwd", "gdn2_layer_gates_bwd",
-           "gdn2_linear_workspace_size", "gdn2_linear_varlen_workspace_size", "gdn2_linear_fwd", "gdn2_linear_bwd", "gdn2_linear_varlen_fwd",
-           "gdn2_linear_varlen_bwd", "gdn2_linear_decode_step", "gdn2_qk_norm_rope_workspace_size",
-           "gdn2_qk_norm_rope_fwd", "gdn2_qk_norm_rope_bwd")
+           "gdn2_linear_workspace_size", "gdn2_linear_varlen_workspace_size", "gdn2_linear_fwd", "gdn2_linear_bwd",
+           "gdn2_linear_varlen_fwd", "gdn2_linear_varlen_bwd", "gdn2_linear_decode_step",
+           "gdn2_qk_norm_rope_workspace_size", "gdn2_qk_norm_rope_fwd", "gdn2_qk_norm_rope_bwd")
 GDN2_GATE_KDA, GDN2_GATE_GDN = 1, 2
 
 
@@ -562,7 +562,8 @@ def gdn2_linear_bwd(q, k, v, log_decay, dout, S0=None, dST=None, want_dS0: bool 
 
 def gdn2_linear_varlen_fwd(q, k, v, log_decay, cu_seqlens, Tmax: int, S0=None, want_state: bool = True,
                            ws: Optional[torch.Tensor] = None, o=None, ST=None):
-    """Packed sequences: q, k, v [Ttot, H, D], cu_seqlens int32 [N + 1] on the device, Tmax >= every length.
+    """Packed sequences: q, k, v [Ttot, H, D], cu_seqlens int32 [N + 1] on the device, Tmax >= every length (a bound above
+    Ttot counts as Ttot). ``ws``: at least ``gdn2_linear_varlen_workspace_size(GDN2_OP_FWD, ...)`` bytes.
     Returns ``(o [Ttot, H, Dv], ST [N, H, Dk, Dv] or None)``; rows of ``o`` behind the last sequence are not written."""
     (o,), ST = _linear("gdn2_linear_varlen_fwd", q, k, v, log_decay, S0, None, None, cu_seqlens, Tmax, want_state, ws,
                        (("o", o, v),), ("ST", ST))
